@@ -165,6 +165,31 @@ typedef struct kvq_compare_t {
   int64_t packed_quantized_bytes;   /* (codes + 1) / 2 + 4 bytes per scale (two codes a byte) */
 } kvq_compare_t;
 
+/* A packed batch of prompts (kvq_prompt_attention, kvq_prompt_weights,
+ * kvq_evict).  Sequence i takes the seq_lens[i] token rows after those of the
+ * sequences before it (0 is allowed); rows of a tensor past the last sequence
+ * are neither read into a result nor written.  Element (token, head, c) of a
+ * tensor is at token * token_stride + head * head_stride + c (strides in
+ * elements, multiples of 16 bytes and at least head_dim; those of a dimension
+ * of one entry are not used), so packed projections, slices of one fused
+ * projection and head-major tensors are all taken as they are. */
+typedef struct kvq_prompt {
+  int32_t n_seqs;       /* >= 1 */
+  int32_t n_q_heads;    /* Hq, a multiple of Hkv with g = Hq / Hkv <= 8 */
+  int32_t n_kv_heads;   /* Hkv >= 1 */
+  int32_t head_dim;     /* d: a multiple of 16, 16 <= d <= 256 */
+  int32_t dtype;        /* kvq_dtype of q, k, v, out and the kept rows */
+  const int64_t* seq_lens; /* host array of n_seqs lengths, read during the call */
+  int64_t n_tokens;     /* token rows the tensors have (>= the lengths' sum, < 2^31) */
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int32_t* status;      /* device word, or NULL: a kernel whose bounded wait gave
+                           up ORs a non-zero code into it (its results are then
+                           undefined); never cleared by the library */
+} kvq_prompt;
+
 typedef struct kvq_cache kvq_cache; /* opaque host handle */
 
 /*
@@ -410,6 +435,53 @@ kvq_status kvq_dense_decode_attention(kvq_cache* cache, const void* k, const voi
 kvq_status kvq_compare(const void* key, const void* value, int64_t batch, int32_t heads, int64_t tokens,
                        int32_t head_dim, kvq_dtype dtype, int32_t qmax, float eps, int32_t group,
                        void* workspace, kvq_compare_t* out, void* stream);
+
+/* Causal attention over whole prompts, before their Keys and Values enter a
+ * cache ("KV Cache 与自回归视频生成", causal attention
+ * softmax(Q K^T / sqrt(d) + M) V, with attn_step's head mapping): for token i of
+ * each sequence and query head h,
+ *   out[i][h] = sum_{j <= i} softmax_j(q[i][h] . k[j][h / g] / sqrt(d)) v[j][h / g],
+ *   lse[h][i] = log sum_{j <= i} exp(q[i][h] . k[j][h / g] / sqrt(d)).
+ * q, out: [n_tokens][n_q_heads][head_dim]; k, v: [n_tokens][n_kv_heads]
+ * [head_dim]; lse: float [n_q_heads][n_tokens] (natural logarithm; may be
+ * NULL).  Scores, softmax statistics and the output sum are fp32; for bf16 the
+ * softmax weights are rounded to bf16 before they meet v.  One sequence's
+ * values never reach another's result, whatever they hold; inside a sequence
+ * finite values are assumed (as everywhere in this library).  out must not
+ * overlap the inputs.  Only enqueues work on ``stream``; needs no workspace, and
+ * two calls may run at once.  Errors before any launch: KVQ_EINVAL (shape,
+ * stride, length, NULL or misaligned pointer, or memory that is not on the
+ * current device), KVQ_EUNSUPPORTED (head_dim, g, strides of 2^40 bytes). */
+kvq_status kvq_prompt_attention(const kvq_prompt* prompt, const void* q, const void* k, const void* v, void* out,
+                                float* lse, void* stream);
+
+/* The attention weight each prompt token has gathered from the last ``last``
+ * queries of its sequence (from all of them when the sequence is no longer):
+ *   weights[hkv][j] = sum over the g query heads h of hkv, over the counted
+ *   tokens i >= j, of exp(q[i][h] . k[j][hkv] / sqrt(d) - lse[h][i]),
+ * with lse as kvq_prompt_attention wrote it for the same prompt (entries of
+ * queries that do not count are not read).  weights: float
+ * [n_kv_heads][n_tokens], every token of every sequence written.  Summed in
+ * fp32 in a fixed order: the same call gives the same bits.  The strides of v
+ * and out are not used.  Errors as kvq_prompt_attention; last >= 1. */
+kvq_status kvq_prompt_weights(const kvq_prompt* prompt, const void* q, const void* k, const float* lse, int64_t last,
+                              float* weights, void* stream);
+
+/* Evict a prompt's light tokens before it is quantized: for every sequence i
+ * and KV head keep keep[i] of its tokens -- the first ``first``, the last
+ * ``recent`` and, of those between, the ones with the largest weights (equal
+ * weights: the lowest token; NaN counts as lowest) -- and gather their Key and
+ * Value rows in token order.  weights: float [n_kv_heads][n_tokens], e.g. of
+ * kvq_prompt_weights.  keep: host array of n_seqs counts, 0 <= keep[i] <=
+ * seq_lens[i], and first + recent <= keep[i] wherever a token goes.  k_out,
+ * v_out receive per sequence a block [n_kv_heads][keep[i]][head_dim], one after
+ * the other: what kvq_append takes for that sequence (n_tokens = keep[i],
+ * n_seqs = 1).  index: int32, the same blocks without head_dim: the kept
+ * tokens' positions in their sequence.  Equal rows come back bit for bit.  The
+ * strides of q and out are not used.  Outputs must not overlap inputs.  Errors
+ * as kvq_prompt_attention. */
+kvq_status kvq_evict(const kvq_prompt* prompt, const void* k, const void* v, const float* weights, const int64_t* keep,
+                     int64_t first, int64_t recent, void* k_out, void* v_out, int32_t* index, void* stream);
 
 /* Size in bytes of one group page for this configuration (0 if invalid). */
 size_t kvq_page_bytes(const kvq_config* cfg);

@@ -24,7 +24,8 @@ EXPORTED = ("kvq_required_bytes", "kvq_create", "kvq_append", "kvq_decode_attent
             "kvq_export_pages", "kvq_device_status", "kvq_page_bytes", "kvq_kernel_launches", "kvq_destroy",
             "kvq_last_error", "kvq_decode_attention_noalloc", "kvq_restore", "kvq_dense_decode_attention",
             "kvq_compare", "kvq_required_bytes_paged", "kvq_create_paged", "kvq_release", "kvq_pool_state",
-            "kvq_required_bytes_segmented", "kvq_create_segmented", "kvq_decode_step")
+            "kvq_required_bytes_segmented", "kvq_create_segmented", "kvq_decode_step",
+            "kvq_prompt_attention", "kvq_prompt_weights", "kvq_evict")
 
 
 class kvq_config(ctypes.Structure):
@@ -57,6 +58,14 @@ class kvq_compare_t(ctypes.Structure):
     _fields_ = [("key_mse", ctypes.c_double), ("value_mse", ctypes.c_double)] + [
         (n, ctypes.c_int64) for n in ("n_key_scales", "n_value_scales", "raw_bytes", "container_quantized_bytes",
                                       "packed_quantized_bytes")]
+
+
+class kvq_prompt(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_q_heads", "n_kv_heads", "head_dim", "dtype")] + [
+        ("seq_lens", ctypes.POINTER(ctypes.c_int64))] + [
+        (n, ctypes.c_int64) for n in ("n_tokens", "q_token_stride", "q_head_stride", "k_token_stride",
+                                      "k_head_stride", "v_token_stride", "v_head_stride", "out_token_stride",
+                                      "out_head_stride")] + [("status", ctypes.c_void_p)]
 
 
 class KVQError(RuntimeError):
@@ -103,6 +112,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvq_create_segmented": ([P(kvq_config), P(I64), V, SZ, P(V)], ctypes.c_int),
         "kvq_release": ([V, I32, I32], ctypes.c_int),
         "kvq_pool_state": ([V, P(I64), P(I64)], ctypes.c_int),
+        "kvq_prompt_attention": ([P(kvq_prompt), V, V, V, V, V, V], ctypes.c_int),
+        "kvq_prompt_weights": ([P(kvq_prompt), V, V, V, I64, V, V], ctypes.c_int),
+        "kvq_evict": ([P(kvq_prompt), V, V, V, P(I64), I64, I64, V, V, V, V], ctypes.c_int),
         "kvq_destroy": ([V], None),
         "kvq_last_error": ([], ctypes.c_char_p),
     }
@@ -272,6 +284,157 @@ def compare(key, value, qmax=7, eps=1e-8, group=0) -> dict:
                        torch.cuda.current_stream(key.device).cuda_stream)
 
 
+def kvq_prompt_attention(prompt: kvq_prompt, q_ptr, k_ptr, v_ptr, out_ptr, lse_ptr, stream) -> None:
+    _check(load_library().kvq_prompt_attention(ctypes.byref(prompt), q_ptr, k_ptr, v_ptr, out_ptr, lse_ptr, stream))
+
+
+def kvq_prompt_weights(prompt: kvq_prompt, q_ptr, k_ptr, lse_ptr, last, weights_ptr, stream) -> None:
+    _check(load_library().kvq_prompt_weights(ctypes.byref(prompt), q_ptr, k_ptr, lse_ptr, last, weights_ptr, stream))
+
+
+def kvq_evict(prompt: kvq_prompt, k_ptr, v_ptr, weights_ptr, keep, first, recent, k_out_ptr, v_out_ptr, index_ptr,
+              stream) -> None:
+    _check(load_library().kvq_evict(ctypes.byref(prompt), k_ptr, v_ptr, weights_ptr, _i64_array(keep), first, recent,
+                                    k_out_ptr, v_out_ptr, index_ptr, stream))
+
+
+# ---- prompt operators on torch tensors ---------------------------------------
+
+_prompt_status = {}  # device index -> int32 status word that the prompt kernels report to
+
+
+def _status_word(device):
+    import torch
+    word = _prompt_status.get(device.index)
+    if word is None and not torch.cuda.is_current_stream_capturing():
+        word = _prompt_status[device.index] = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.synchronize(device)  # cleared before any stream can report to it
+    return word  # None in a capture that no eager call came before: those kernels report nowhere
+
+
+def prompt_status(device=None) -> int:
+    """The prompt kernels' status word on a device (synchronizes): 0 unless a
+    bounded wait gave up there since the process started."""
+    import torch
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        return int(_status_word(torch.device("cuda", torch.cuda.current_device())).item())
+
+
+def _check_packed(name, t, like=None):
+    assert t.is_cuda and t.dim() == 3, f"{name} must be a CUDA tensor [tokens, heads, head_dim]"
+    assert t.stride(2) == 1 or t.shape[2] == 1, f"{name}'s last dimension must be contiguous"
+    if like is not None:
+        assert t.device == like.device and t.dtype == like.dtype, f"{name} must match the device and dtype of k"
+        assert t.shape[0] == like.shape[0] and t.shape[2] == like.shape[2], \
+            f"{name} must have k's tokens and head_dim, got {tuple(t.shape)}"
+
+
+def _prompt(k, seq_lens, q=None, v=None, out=None):
+    import torch
+    _check_packed("k", k)
+    dtypes = {torch.bfloat16: KVQ_BF16, torch.float32: KVQ_FP32}
+    assert k.dtype in dtypes, f"expected bfloat16 or float32, got {k.dtype}"
+    lens = _i64_array(seq_lens)
+    p = kvq_prompt(len(lens), k.shape[1], k.shape[1], k.shape[2], dtypes[k.dtype], lens, k.shape[0])
+    p.k_token_stride, p.k_head_stride = k.stride(0), k.stride(1)
+    if q is not None:
+        _check_packed("q", q, k)
+        p.n_q_heads, p.q_token_stride, p.q_head_stride = q.shape[1], q.stride(0), q.stride(1)
+    if v is not None:
+        _check_packed("v", v, k)
+        assert v.shape == k.shape, f"v must have k's shape, got {tuple(v.shape)}"
+        p.v_token_stride, p.v_head_stride = v.stride(0), v.stride(1)
+    if out is not None:
+        _check_packed("out", out, k)
+        assert out.shape == q.shape, f"out must have q's shape, got {tuple(out.shape)}"
+        p.out_token_stride, p.out_head_stride = out.stride(0), out.stride(1)
+    word = _status_word(k.device)
+    p.status = None if word is None else word.data_ptr()
+    return p
+
+
+def _check_rows(name, t, rows, k):
+    assert t.device == k.device and t.is_contiguous() and str(t.dtype) == "torch.float32", \
+        f"{name} must be a contiguous float32 tensor on k's device"
+    assert tuple(t.shape) == (rows, k.shape[0]), f"expected {name} of shape {(rows, k.shape[0])}, got {tuple(t.shape)}"
+
+
+def prompt_attention(q, k, v, seq_lens, out=None, lse=None):
+    """Causal attention over packed prompts: q [tokens, n_q_heads, head_dim],
+    k, v [tokens, n_kv_heads, head_dim] (bf16 or fp32; any strides of whole
+    16-byte steps), seq_lens the sequences' lengths in order.  Returns (out,
+    lse): out like q, lse float32 [n_q_heads, tokens]."""
+    import torch
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    p = _prompt(k, seq_lens, q, v, out)
+    if lse is None:
+        lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+    else:
+        _check_rows("lse", lse, q.shape[1], k)
+    with torch.cuda.device(k.device):
+        kvq_prompt_attention(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                             torch.cuda.current_stream(k.device).cuda_stream)
+    return out, lse
+
+
+def prompt_weights(q, k, lse, seq_lens, last, out=None):
+    """The attention weight every prompt token gathers from the last ``last``
+    queries of its sequence, summed over the query heads of its KV head
+    (float32 [n_kv_heads, tokens]); lse as prompt_attention returned it."""
+    import torch
+    p = _prompt(k, seq_lens, q)
+    _check_rows("lse", lse, q.shape[1], k)
+    if out is None:
+        out = torch.empty(k.shape[1], k.shape[0], dtype=torch.float32, device=k.device)
+    else:
+        _check_rows("out", out, k.shape[1], k)
+    with torch.cuda.device(k.device):
+        kvq_prompt_weights(p, q.data_ptr(), k.data_ptr(), lse.data_ptr(), last, out.data_ptr(),
+                           torch.cuda.current_stream(k.device).cuda_stream)
+    return out
+
+
+class Kept:
+    """What evict kept.  k, v [rows, head_dim] and index [rows] hold one block
+    [n_kv_heads, counts[i]] per sequence, back to back."""
+
+    def __init__(self, k, v, index, counts, n_kv_heads):
+        self.k, self.v, self.index, self.counts, self.n_kv_heads = k, v, index, counts, n_kv_heads
+
+    def sequence(self, i):
+        """(k, v, index) of sequence i: k, v [1, n_kv_heads, counts[i],
+        head_dim] as KVQCache.append takes them, index [n_kv_heads, counts[i]]
+        (positions in the sequence, rising)."""
+        at, n = sum(self.counts[:i]) * self.n_kv_heads, self.counts[i]
+        rows = slice(at, at + n * self.n_kv_heads)
+        shape = (1, self.n_kv_heads, n, self.k.shape[1])
+        return self.k[rows].view(shape), self.v[rows].view(shape), self.index[rows].view(self.n_kv_heads, n)
+
+
+def evict(k, v, weights, seq_lens, keep, first=0, recent=0):
+    """Keep ``keep`` tokens of every sequence and KV head (an int, cut to each
+    sequence's length, or a count per sequence): the first ``first``, the last
+    ``recent`` and the heaviest between, equal weights by lowest token.  k, v
+    [tokens, n_kv_heads, head_dim]; weights float32 [n_kv_heads, tokens].
+    Returns a Kept."""
+    import torch
+    p = _prompt(k, seq_lens, v=v)
+    _check_rows("weights", weights, k.shape[1], k)
+    lens = list(seq_lens)
+    counts = [min(int(keep), int(n)) for n in lens] if isinstance(keep, int) else [int(n) for n in keep]
+    assert len(counts) == len(lens), f"expected {len(lens)} counts in keep, got {len(counts)}"
+    rows = max(0, sum(counts)) * k.shape[1]
+    k_out = torch.empty(rows, k.shape[2], dtype=k.dtype, device=k.device)
+    v_out = torch.empty_like(k_out)
+    index = torch.empty(rows, dtype=torch.int32, device=k.device)
+    with torch.cuda.device(k.device):
+        kvq_evict(p, k.data_ptr(), v.data_ptr(), weights.data_ptr(), counts, first, recent, k_out.data_ptr(),
+                  v_out.data_ptr(), index.data_ptr(), torch.cuda.current_stream(k.device).cuda_stream)
+    return Kept(k_out, v_out, index, counts, k.shape[1])
+
+
 def kvq_kernel_launches() -> int:
     return load_library().kvq_kernel_launches()
 
@@ -337,6 +500,13 @@ class KVQCache:
         self._check_input(new_k, shape)
         self._check_input(new_v, shape)
         kvq_append(self.handle, new_k.data_ptr(), new_v.data_ptr(), n, seq_begin, n_seqs, self._stream())
+
+    def append_kept(self, kept, seq_begin=0):
+        """Append what evict kept: its sequence i to sequence seq_begin + i."""
+        for i, n in enumerate(kept.counts):
+            if n:
+                k, v, _ = kept.sequence(i)
+                self.append(k, v, seq_begin + i)
 
     def decode_attention(self, q, out=None, kernel=0, chunk_pages=0, split_start=None, split_stop=None):
         """q: [batch, n_q_heads, head_dim]; returns float32 [batch, n_q_heads, head_dim]."""

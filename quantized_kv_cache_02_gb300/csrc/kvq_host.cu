@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "../../include/kvq.h"
+#include "kvq_host.h"
 #include "kvq_internal.h"
 
 using kvq::SeqCounters;
@@ -70,6 +71,10 @@ namespace {
 thread_local std::string g_err;
 std::atomic<uint64_t> g_launches{0};
 
+}  // namespace
+
+namespace kvq {
+
 kvq_status fail(kvq_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -83,6 +88,15 @@ kvq_status fail(kvq_status st, const char* fmt, ...) {
 kvq_status cuda_fail(cudaError_t e, const char* what) {
   return fail(KVQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+void count_launches(uint64_t n) { g_launches += n; }
+
+}  // namespace kvq
+
+namespace {
+
+using kvq::cuda_fail;
+using kvq::fail;
 
 constexpr int64_t kMinChunkTokens = 256;
 constexpr size_t kAlign = 256;

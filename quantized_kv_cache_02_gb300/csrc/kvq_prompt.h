@@ -1,0 +1,91 @@
+// Internal definitions of the prompt operators (kvq_prompt_attention,
+// kvq_prompt_weights, kvq_evict): launch parameter blocks, the order in which
+// a launch takes its tiles, and the launchers.
+#pragma once
+
+#include "kvq_internal.h"
+
+namespace kvq {
+
+// Device status word bit of the prompt kernels.
+constexpr int32_t kStatusPromptTimeout = 0x102;  // a bounded mbarrier wait gave up
+
+struct PromptSeq {
+  int32_t start;  // first token row
+  int32_t len;
+};
+
+// Tiles of one launch.  Sequence s (sorted by falling length) is cut into
+// nb[s] = ceil(len / step) blocks of ``step`` tokens.  Block costs grow along a
+// sequence (causal), so tiles are taken level by level from the top: level l
+// holds block l of every sequence that has one, times the KV heads.  Segment k
+// is the levels that exactly the first k + 1 sequences reach; first[k] is its
+// first tile.
+struct PromptTiles {
+  int32_t n_seqs, Hkv, step;
+  int64_t first[kMaxSeqsPerLaunch + 1];
+  PromptSeq seq[kMaxSeqsPerLaunch];
+};
+
+__host__ __device__ inline int prompt_blocks(int len, int step) { return (int)(((int64_t)len + step - 1) / step); }
+
+// Tile x: its sequence (index into seq), KV head and level.
+__host__ __device__ inline void prompt_tile(const PromptTiles& t, int64_t x, int* seq, int* head, int* level) {
+  int lo = 0, hi = t.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.first[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t off = x - t.first[lo], per = (int64_t)(lo + 1) * t.Hkv;
+  const int down = (int)(off / per), rem = (int)(off - down * per);
+  *level = prompt_blocks(t.seq[lo].len, t.step) - 1 - down;
+  *seq = rem / t.Hkv;
+  *head = rem - *seq * t.Hkv;
+}
+
+struct PromptParams {
+  int32_t D, Hq, Hkv, g;
+  float scale2;                // log2(e) / sqrt(D): scores are kept in base 2
+  const void* q;               // element (token, head, c) at token * q_ts + head * q_hs + c
+  const void* k;
+  const void* v;
+  void* out;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
+  float* lse;                  // [Hq][n_tokens] (attention: written if non-null; weights: read)
+  float* weights;              // [Hkv][n_tokens]
+  int64_t n_tokens;
+  int64_t last;                // weights: queries counted back from each sequence's end
+  int32_t* status;
+  PromptTiles tiles;
+};
+
+struct EvictSeq {
+  int64_t out_row;             // rows (of every KV head) before this sequence's
+  int32_t start, len, keep;
+};
+
+struct EvictParams {
+  int32_t Hkv, row_bytes;      // bytes of one token's head
+  int32_t first, recent;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t k_ts, k_hs, v_ts, v_hs;  // bytes
+  const float* weights;        // [Hkv][n_tokens]
+  int64_t n_tokens;
+  uint8_t* k_out;              // per sequence [Hkv][keep][row_bytes]
+  uint8_t* v_out;
+  int32_t* index;              // per sequence [Hkv][keep]
+  int32_t n_seqs;
+  EvictSeq seq[kMaxSeqsPerLaunch];
+};
+
+// Launchers (return the launch's error code).
+cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
+cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
+cudaError_t launch_evict(const EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s);
+
+// Rows of a CUDA-core attention tile and keys of one of its steps.
+constexpr int kPromptRows = 64, kPromptKeys = 64;
+
+}  // namespace kvq

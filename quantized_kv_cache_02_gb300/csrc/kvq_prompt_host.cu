@@ -1,0 +1,312 @@
+// Host side of the prompt operators: argument checks, tile order and launches
+// of kvq_prompt_attention, kvq_prompt_weights and kvq_evict.  Sequence lengths
+// live on the host and travel in the launch parameter block, so no call
+// synchronizes with the device or needs a workspace.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "kvq_host.h"
+#include "kvq_prompt.h"
+
+namespace {
+
+using kvq::cuda_fail;
+using kvq::fail;
+
+constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
+
+int esize_of(const kvq_prompt* p) { return p->dtype == KVQ_BF16 ? 2 : 4; }
+
+// Shapes and lengths; *total receives the sum of the lengths.
+kvq_status check_prompt(const kvq_prompt* p, int64_t* total) {
+  if (!p) return fail(KVQ_EINVAL, "prompt is NULL");
+  if (p->n_seqs < 1) return fail(KVQ_EINVAL, "n_seqs must be >= 1 (got %d)", p->n_seqs);
+  if (p->n_kv_heads < 1) return fail(KVQ_EINVAL, "n_kv_heads must be >= 1");
+  if (p->n_kv_heads > 65535) return fail(KVQ_EUNSUPPORTED, "n_kv_heads must be <= 65535");
+  if (p->n_q_heads < 1 || p->n_q_heads % p->n_kv_heads != 0)
+    return fail(KVQ_EINVAL, "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d)", p->n_q_heads,
+                p->n_kv_heads);
+  if (p->n_q_heads / p->n_kv_heads > kvq::kMaxGqa)
+    return fail(KVQ_EUNSUPPORTED, "query heads per KV head must be <= %d", kvq::kMaxGqa);
+  if (p->head_dim < 16 || p->head_dim > 256 || p->head_dim % 16 != 0)
+    return fail(KVQ_EUNSUPPORTED, "head_dim must be a multiple of 16 in [16, 256] (got %d)", p->head_dim);
+  if (p->dtype != KVQ_BF16 && p->dtype != KVQ_FP32) return fail(KVQ_EINVAL, "unknown dtype %d", p->dtype);
+  if (!p->seq_lens) return fail(KVQ_EINVAL, "seq_lens is NULL");
+  if (p->n_tokens < 0 || p->n_tokens >= (int64_t(1) << 31))
+    return fail(KVQ_EINVAL, "n_tokens must be in [0, 2^31) (got %lld)", (long long)p->n_tokens);
+  int64_t sum = 0;
+  for (int i = 0; i < p->n_seqs; ++i) {
+    if (p->seq_lens[i] < 0 || p->seq_lens[i] > p->n_tokens - sum)
+      return fail(KVQ_EINVAL, "length %lld of sequence %d is negative or goes past the %lld token rows",
+                  (long long)p->seq_lens[i], i, (long long)p->n_tokens);
+    sum += p->seq_lens[i];
+  }
+  *total = sum;
+  return KVQ_OK;
+}
+
+// A [tokens][heads][head_dim] tensor: strides in elements, 16-byte steps.
+kvq_status check_tensor(const kvq_prompt* p, const char* name, const void* ptr, int64_t ts, int64_t hs, int heads) {
+  if (!ptr || ((uintptr_t)ptr & 15u))
+    return fail(KVQ_EINVAL, "%s must be a non-NULL 16-byte aligned device pointer", name);
+  const int64_t step = 16 / esize_of(p);
+  if ((p->n_tokens > 1 && (ts < p->head_dim || ts % step)) || (heads > 1 && (hs < p->head_dim || hs % step)))
+    return fail(KVQ_EINVAL, "%s strides (token %lld, head %lld) must be multiples of %lld elements and at least head_dim",
+                name, (long long)ts, (long long)hs, (long long)step);
+  if (std::max(ts, hs) >= (int64_t(1) << 40) / esize_of(p))
+    return fail(KVQ_EUNSUPPORTED, "%s strides must be below 2^40 bytes", name);
+  return KVQ_OK;
+}
+
+// Kernels launch on the current device: every tensor has to live there.
+kvq_status check_on_device(const char* name, const void* ptr) {
+  int cur = -1;
+  cudaError_t e = cudaGetDevice(&cur);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  cudaPointerAttributes attr;
+  e = cudaPointerGetAttributes(&attr, ptr);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes");
+  if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged)
+    return fail(KVQ_EINVAL, "%s is not device memory", name);
+  if (attr.type == cudaMemoryTypeDevice && attr.device != cur)
+    return fail(KVQ_EINVAL, "the current device is %d but %s lives on device %d", cur, name, attr.device);
+  return KVQ_OK;
+}
+
+kvq_status check_floats(const char* name, const void* ptr) {
+  if (!ptr || ((uintptr_t)ptr & 3u)) return fail(KVQ_EINVAL, "%s must be a non-NULL 4-byte aligned device pointer", name);
+  return check_on_device(name, ptr);
+}
+
+kvq_status check_status_word(const kvq_prompt* p) { return p->status ? check_floats("status", p->status) : KVQ_OK; }
+
+#define KVQ_TRY(x)                       \
+  do {                                   \
+    const kvq_status st_ = (x);          \
+    if (st_ != KVQ_OK) return st_;       \
+  } while (0)
+
+// The sequences of the prompt that hold tokens, in launches of at most
+// kMaxSeqsPerLaunch, each sorted by falling length.
+std::vector<std::vector<kvq::PromptSeq>> launches_of(const kvq_prompt* p) {
+  std::vector<std::vector<kvq::PromptSeq>> out;
+  int64_t start = 0;
+  for (int i = 0; i < p->n_seqs; ++i) {
+    const int64_t n = p->seq_lens[i];
+    if (n > 0) {
+      if (out.empty() || (int)out.back().size() == kvq::kMaxSeqsPerLaunch) out.emplace_back();
+      out.back().push_back({(int32_t)start, (int32_t)n});
+    }
+    start += n;
+  }
+  for (auto& l : out)
+    std::stable_sort(l.begin(), l.end(), [](const kvq::PromptSeq& a, const kvq::PromptSeq& b) { return a.len > b.len; });
+  return out;
+}
+
+// Tiles of ``step`` tokens over the sequences; returns their number.
+int64_t fill_tiles(const std::vector<kvq::PromptSeq>& seqs, int hkv, int step, kvq::PromptTiles* t) {
+  t->n_seqs = (int32_t)seqs.size();
+  t->Hkv = hkv;
+  t->step = step;
+  int64_t x = 0;
+  for (int k = 0; k < t->n_seqs; ++k) {
+    t->seq[k] = seqs[k];
+    t->first[k] = x;
+    const int64_t below = k + 1 < t->n_seqs ? kvq::prompt_blocks(seqs[k + 1].len, step) : 0;
+    x += (kvq::prompt_blocks(seqs[k].len, step) - below) * (int64_t)(k + 1) * hkv;
+  }
+  t->first[t->n_seqs] = x;
+  return x;
+}
+
+void base_params(const kvq_prompt* p, kvq::PromptParams* pp) {
+  memset(pp, 0, sizeof *pp);
+  pp->D = p->head_dim;
+  pp->Hq = p->n_q_heads;
+  pp->Hkv = p->n_kv_heads;
+  pp->g = p->n_q_heads / p->n_kv_heads;
+  pp->scale2 = (float)(1.4426950408889634 / std::sqrt((double)p->head_dim));
+  pp->q_ts = p->q_token_stride;
+  pp->q_hs = p->q_head_stride;
+  pp->k_ts = p->k_token_stride;
+  pp->k_hs = p->k_head_stride;
+  pp->v_ts = p->v_token_stride;
+  pp->v_hs = p->v_head_stride;
+  pp->o_ts = p->out_token_stride;
+  pp->o_hs = p->out_head_stride;
+  pp->n_tokens = p->n_tokens;
+  pp->status = p->status;
+}
+
+kvq_status prompt_attention(const kvq_prompt* p, const void* q, const void* k, const void* v, void* out, float* lse,
+                            void* stream) {
+  int64_t total = 0;
+  KVQ_TRY(check_prompt(p, &total));
+  if (total == 0) return KVQ_OK;
+  KVQ_TRY(check_tensor(p, "q", q, p->q_token_stride, p->q_head_stride, p->n_q_heads));
+  KVQ_TRY(check_tensor(p, "k", k, p->k_token_stride, p->k_head_stride, p->n_kv_heads));
+  KVQ_TRY(check_tensor(p, "v", v, p->v_token_stride, p->v_head_stride, p->n_kv_heads));
+  KVQ_TRY(check_tensor(p, "out", out, p->out_token_stride, p->out_head_stride, p->n_q_heads));
+  KVQ_TRY(check_on_device("q", q));
+  KVQ_TRY(check_on_device("k", k));
+  KVQ_TRY(check_on_device("v", v));
+  KVQ_TRY(check_on_device("out", out));
+  if (lse) KVQ_TRY(check_floats("lse", lse));
+  KVQ_TRY(check_status_word(p));
+  kvq::PromptParams pp;
+  base_params(p, &pp);
+  pp.q = q;
+  pp.k = k;
+  pp.v = v;
+  pp.out = out;
+  pp.lse = lse;
+  const int step = kvq::kPromptRows / pp.g;
+  const auto launches = launches_of(p);
+  for (const auto& l : launches)
+    if (fill_tiles(l, pp.Hkv, step, &pp.tiles) > kMaxTiles) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
+  for (const auto& l : launches) {
+    const int64_t tiles = fill_tiles(l, pp.Hkv, step, &pp.tiles);
+    const cudaError_t e =
+        kvq::launch_prompt_simt(pp, p->dtype == KVQ_BF16 ? 0 : 1, tiles, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+    kvq::count_launches(1);
+  }
+  return KVQ_OK;
+}
+
+kvq_status prompt_weights(const kvq_prompt* p, const void* q, const void* k, const float* lse, int64_t last,
+                          float* weights, void* stream) {
+  int64_t total = 0;
+  KVQ_TRY(check_prompt(p, &total));
+  if (last < 1) return fail(KVQ_EINVAL, "last must be >= 1 (got %lld)", (long long)last);
+  if (total == 0) return KVQ_OK;
+  KVQ_TRY(check_tensor(p, "q", q, p->q_token_stride, p->q_head_stride, p->n_q_heads));
+  KVQ_TRY(check_tensor(p, "k", k, p->k_token_stride, p->k_head_stride, p->n_kv_heads));
+  KVQ_TRY(check_on_device("q", q));
+  KVQ_TRY(check_on_device("k", k));
+  KVQ_TRY(check_floats("lse", lse));
+  KVQ_TRY(check_floats("weights", weights));
+  KVQ_TRY(check_status_word(p));
+  kvq::PromptParams pp;
+  base_params(p, &pp);
+  pp.q = q;
+  pp.k = k;
+  pp.lse = const_cast<float*>(lse);
+  pp.weights = weights;
+  pp.last = last;
+  const auto launches = launches_of(p);
+  for (const auto& l : launches)
+    if (fill_tiles(l, pp.Hkv, kvq::kPromptKeys, &pp.tiles) > kMaxTiles)
+      return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
+  for (const auto& l : launches) {
+    const int64_t tiles = fill_tiles(l, pp.Hkv, kvq::kPromptKeys, &pp.tiles);
+    const cudaError_t e =
+        kvq::launch_weights_simt(pp, p->dtype == KVQ_BF16 ? 0 : 1, tiles, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prompt weights launch");
+    kvq::count_launches(1);
+  }
+  return KVQ_OK;
+}
+
+kvq_status evict(const kvq_prompt* p, const void* k, const void* v, const float* weights, const int64_t* keep,
+                 int64_t first, int64_t recent, void* k_out, void* v_out, int32_t* index, void* stream) {
+  int64_t total = 0;
+  KVQ_TRY(check_prompt(p, &total));
+  if (!keep) return fail(KVQ_EINVAL, "keep is NULL");
+  if (first < 0 || recent < 0)
+    return fail(KVQ_EINVAL, "first (%lld) and recent (%lld) must not be negative", (long long)first, (long long)recent);
+  int64_t kept = 0;
+  for (int i = 0; i < p->n_seqs; ++i) {
+    if (keep[i] < 0 || keep[i] > p->seq_lens[i])
+      return fail(KVQ_EINVAL, "keep[%d] = %lld is outside [0, %lld]", i, (long long)keep[i], (long long)p->seq_lens[i]);
+    if (keep[i] < p->seq_lens[i] && (first > keep[i] || recent > keep[i] - first))
+      return fail(KVQ_EINVAL, "sequence %d keeps %lld tokens, fewer than its first %lld and last %lld", i,
+                  (long long)keep[i], (long long)first, (long long)recent);
+    kept += keep[i];
+  }
+  if (kept == 0) return KVQ_OK;
+  KVQ_TRY(check_tensor(p, "k", k, p->k_token_stride, p->k_head_stride, p->n_kv_heads));
+  KVQ_TRY(check_tensor(p, "v", v, p->v_token_stride, p->v_head_stride, p->n_kv_heads));
+  if (!k_out || !v_out || ((uintptr_t)k_out & 15u) || ((uintptr_t)v_out & 15u))
+    return fail(KVQ_EINVAL, "k_out / v_out must be non-NULL 16-byte aligned device pointers");
+  KVQ_TRY(check_on_device("k", k));
+  KVQ_TRY(check_on_device("v", v));
+  KVQ_TRY(check_on_device("k_out", k_out));
+  KVQ_TRY(check_on_device("v_out", v_out));
+  KVQ_TRY(check_floats("weights", weights));
+  KVQ_TRY(check_floats("index", index));
+  const int es = esize_of(p);
+  kvq::EvictParams ep;
+  memset(&ep, 0, sizeof ep);
+  ep.Hkv = p->n_kv_heads;
+  ep.row_bytes = p->head_dim * es;
+  // neither can pass a length that evicts, and a sequence that keeps everything reads neither
+  ep.first = (int32_t)std::min<int64_t>(first, p->n_tokens);
+  ep.recent = (int32_t)std::min<int64_t>(recent, p->n_tokens);
+  ep.k = static_cast<const uint8_t*>(k);
+  ep.v = static_cast<const uint8_t*>(v);
+  ep.k_ts = p->k_token_stride * es;
+  ep.k_hs = p->k_head_stride * es;
+  ep.v_ts = p->v_token_stride * es;
+  ep.v_hs = p->v_head_stride * es;
+  ep.weights = weights;
+  ep.n_tokens = p->n_tokens;
+  ep.k_out = static_cast<uint8_t*>(k_out);
+  ep.v_out = static_cast<uint8_t*>(v_out);
+  ep.index = index;
+  int64_t start = 0, row = 0;
+  for (int i = 0; i < p->n_seqs;) {
+    ep.n_seqs = 0;
+    int32_t max_len = 0, max_keep = 0;
+    for (; i < p->n_seqs && ep.n_seqs < kvq::kMaxSeqsPerLaunch; ++i) {
+      if (keep[i] > 0) {
+        ep.seq[ep.n_seqs++] = {row, (int32_t)start, (int32_t)p->seq_lens[i], (int32_t)keep[i]};
+        max_len = std::max(max_len, (int32_t)p->seq_lens[i]);
+        max_keep = std::max(max_keep, (int32_t)keep[i]);
+      }
+      start += p->seq_lens[i];
+      row += keep[i] * p->n_kv_heads;
+    }
+    if (ep.n_seqs == 0) continue;
+    const cudaError_t e = kvq::launch_evict(ep, max_len, max_keep, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "evict launch");
+    kvq::count_launches(2);
+  }
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_prompt_attention(const kvq_prompt* prompt, const void* q, const void* k, const void* v, void* out,
+                                float* lse, void* stream) {
+  try {
+    return prompt_attention(prompt, q, k, v, out, lse, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(KVQ_ENOMEM, "out of host memory");
+  }
+}
+
+kvq_status kvq_prompt_weights(const kvq_prompt* prompt, const void* q, const void* k, const float* lse, int64_t last,
+                              float* weights, void* stream) {
+  try {
+    return prompt_weights(prompt, q, k, lse, last, weights, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(KVQ_ENOMEM, "out of host memory");
+  }
+}
+
+kvq_status kvq_evict(const kvq_prompt* prompt, const void* k, const void* v, const float* weights, const int64_t* keep,
+                     int64_t first, int64_t recent, void* k_out, void* v_out, int32_t* index, void* stream) {
+  return evict(prompt, k, v, weights, keep, first, recent, k_out, v_out, index, stream);
+}
+
+}  // extern "C"

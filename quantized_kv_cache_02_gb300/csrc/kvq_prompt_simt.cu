@@ -1,0 +1,287 @@
+// CUDA-core kernels of the prompt operators: any supported shape and dtype
+// (the tensor-core kernels take bf16 with head_dim 64 and 128).
+//
+// Both work on tiles of 64 rows x 64 keys in fp32.  A row is a (token, query
+// head) pair of one KV head, token major, so the heads that share a KV head
+// share its tiles: 64 / g tokens a tile.  256 threads as 16 x 16; thread
+// (ty, tx) holds rows 4 ty .. 4 ty + 3 and keys tx, tx + 16, tx + 32, tx + 48.
+//
+//   attention:  o_i = sum_{j <= i} p_ij v_j / l_i,  p_ij = 2^(s_ij - m_i),
+//               s_ij = q_i . k_j log2(e) / sqrt(d), one pass over the keys with
+//               the running maximum m and sum l ("KV Cache 与自回归视频生成",
+//               attn_full in section 04's appendix, softmax(QK^T / sqrt(d) + M) V)
+//   weights:    w_j = sum over the last queries i >= j of 2^(s_ij - lse_i)
+//
+// Bound: FMA issue.  Per four channels a thread does 64 FMAs for 8 16-byte
+// shared loads (12 wavefronts a warp against 16 cycles of FMA).
+
+#include <cuda_bf16.h>
+
+#include "kvq_prompt.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPStride = kPromptKeys + 4;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
+// Rows [0, 64) of K or V (keys ``key0`` on of one head) into shared memory as
+// fp32 rows of ``stride`` floats; keys at or past ``end`` and channels past D are 0.
+template <typename T>
+__device__ __forceinline__ void load_keys(float* dst, int stride, int cols, const T* base, int64_t ts, int key0,
+                                          int end, int D) {
+  const int per = cols / 4;
+  for (int i = threadIdx.x; i < kPromptKeys * per; i += kThreads) {
+    const int r = i / per, c = (i - r * per) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key0 + r < end && c < D) x = load4(base + (int64_t)(key0 + r) * ts + c);
+    *reinterpret_cast<float4*>(dst + r * stride + c) = x;
+  }
+}
+
+// Row r of a query tile is token tok0 + r / g, head h * g + r % g; rows past
+// the tile's tokens or the sequence are 0.
+template <typename T>
+__device__ __forceinline__ void load_queries(float* dst, int stride, const PromptParams& p, const T* q, int tok0,
+                                             int tile_tok, int len, int h) {
+  const int per = p.D / 4;
+  for (int i = threadIdx.x; i < kPromptRows * per; i += kThreads) {
+    const int r = i / per, c = (i - r * per) * 4, t = r / p.g;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < tile_tok && tok0 + t < len)
+      x = load4(q + (int64_t)(tok0 + t) * p.q_ts + (int64_t)(h * p.g + r - t * p.g) * p.q_hs + c);
+    *reinterpret_cast<float4*>(dst + r * stride + c) = x;
+  }
+}
+
+__device__ __forceinline__ void scores(float (&s)[4][4], const float* qs, const float* ks, int stride, int D, int ty,
+                                       int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < D; c += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = load4(qs + (4 * ty + i) * stride + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = load4(ks + (tx + 16 * j) * stride + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+      }
+  }
+}
+
+// NC: 64-channel column groups of the output (D <= 64 NC).
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ PromptParams p) {
+  extern __shared__ __align__(16) float simt_smem[];
+  constexpr int kStride = 64 * NC + 4;
+  float* qs = simt_smem;                        // [64][kStride]
+  float* ks = qs + kPromptRows * kStride;       // K, then V
+  float* ps = ks + kPromptKeys * kStride;       // [64][kPStride]
+  int si, h, level;
+  prompt_tile(p.tiles, blockIdx.x, &si, &h, &level);
+  const PromptSeq sq = p.tiles.seq[si];
+  const int tile_tok = p.tiles.step, tok0 = level * tile_tok;
+  const T* q = static_cast<const T*>(p.q) + (int64_t)sq.start * p.q_ts;
+  const T* k = static_cast<const T*>(p.k) + (int64_t)sq.start * p.k_ts + (int64_t)h * p.k_hs;
+  const T* v = static_cast<const T*>(p.v) + (int64_t)sq.start * p.v_ts + (int64_t)h * p.v_hs;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  pdl_wait();
+  pdl_release();
+  load_queries(qs, kStride, p, q, tok0, tile_tok, sq.len, h);
+  const int end = min(sq.len, tok0 + tile_tok);  // keys some row sees
+  float o[NC][4][4], m[4], l[4];
+  int pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    pos[i] = tok0 + (4 * ty + i) / p.g;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[c][i][j] = 0.f;
+  }
+  for (int k0 = 0; k0 < end; k0 += kPromptKeys) {
+    __syncthreads();  // the previous step's V has been read
+    load_keys(ks, kStride, p.D, k, p.k_ts, k0, end, p.D);
+    __syncthreads();
+    float s[4][4];
+    scores(s, qs, ks, kStride, p.D, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = k0 + tx + 16 * j;
+        s[i][j] = key <= pos[i] && key < end ? s[i][j] * p.scale2 : -INFINITY;
+        mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      // key 0 is in every row's first step, so the maximum is finite from then on
+      const float mn = fmaxf(m[i], mx), a = exp2f(m[i] - mn);
+      m[i] = mn;
+      float sum = 0.f;
+      float* row = ps + (4 * ty + i) * kPStride;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2f(s[i][j] - mn);
+        sum += e;
+        row[tx + 16 * j] = e;
+      }
+      l[i] = fmaf(l[i], a, sum);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[c][i][j] *= a;
+    }
+    __syncthreads();  // K has been read; P is complete
+    load_keys(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D);
+    __syncthreads();
+#pragma unroll 2
+    for (int n = 0; n < kPromptKeys; n += 4) {
+      float4 pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = load4(ps + (4 * ty + i) * kPStride + n);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int nn = 0; nn < 4; ++nn) {
+          const float4 vv = load4(ks + (n + nn) * kStride + 64 * c + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float pp = nn == 0 ? pr[i].x : nn == 1 ? pr[i].y : nn == 2 ? pr[i].z : pr[i].w;
+            o[c][i][0] = fmaf(pp, vv.x, o[c][i][0]);
+            o[c][i][1] = fmaf(pp, vv.y, o[c][i][1]);
+            o[c][i][2] = fmaf(pp, vv.z, o[c][i][2]);
+            o[c][i][3] = fmaf(pp, vv.w, o[c][i][3]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i, t = r / p.g, head = h * p.g + r - t * p.g;
+    float lt = l[i];
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
+    if (t >= tile_tok || tok0 + t >= sq.len) continue;
+    const float inv = 1.f / lt;
+    T* dst = static_cast<T*>(p.out) + (int64_t)(sq.start + tok0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = 64 * c + 4 * tx;
+      if (col < p.D)
+        store4(dst + col, make_float4(o[c][i][0] * inv, o[c][i][1] * inv, o[c][i][2] * inv, o[c][i][3] * inv));
+    }
+    if (p.lse && tx == 0)
+      p.lse[(int64_t)head * p.n_tokens + sq.start + tok0 + t] = (m[i] + log2f(lt)) * 0.69314718055994530942f;
+  }
+}
+
+// One CTA per 64 keys of a KV head: the column sums stay in registers while
+// the counted queries pass, so no partial leaves the CTA and the order of
+// every sum is fixed.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_constant__ PromptParams p) {
+  extern __shared__ __align__(16) float simt_smem[];
+  const int stride = p.D + 4;
+  float* qs = simt_smem;
+  float* ks = qs + kPromptRows * stride;
+  float* red = ks + kPromptKeys * stride;  // [16][64]
+  int si, h, level;
+  prompt_tile(p.tiles, blockIdx.x, &si, &h, &level);
+  const PromptSeq sq = p.tiles.seq[si];
+  const int k0 = (prompt_blocks(sq.len, kPromptKeys) - 1 - level) * kPromptKeys;
+  const int tile_tok = kPromptRows / p.g;
+  const T* q = static_cast<const T*>(p.q) + (int64_t)sq.start * p.q_ts;
+  const T* k = static_cast<const T*>(p.k) + (int64_t)sq.start * p.k_ts + (int64_t)h * p.k_hs;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  pdl_wait();
+  pdl_release();
+  load_keys(ks, stride, p.D, k, p.k_ts, k0, sq.len, p.D);
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t back = sq.len - p.last;
+  const int t_first = (int)(back > k0 ? back : k0);
+  for (int t0 = t_first; t0 < sq.len; t0 += tile_tok) {
+    __syncthreads();
+    load_queries(qs, stride, p, q, t0, tile_tok, sq.len, h);
+    __syncthreads();
+    float s[4][4];
+    scores(s, qs, ks, stride, p.D, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * ty + i, t = r / p.g, pos = t0 + t;
+      if (t < tile_tok && pos < sq.len) {
+        const float lse2 =
+            p.lse[(int64_t)(h * p.g + r - t * p.g) * p.n_tokens + sq.start + pos] * 1.44269504088896340736f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k0 + tx + 16 * j <= pos) sum[j] += exp2f(fmaf(s[i][j], p.scale2, -lse2));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[ty * 64 + tx + 16 * j] = sum[j];
+  __syncthreads();
+  if (threadIdx.x < kPromptKeys && k0 + threadIdx.x < sq.len) {
+    float w = 0.f;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) w += red[y * 64 + threadIdx.x];
+    p.weights[(int64_t)h * p.n_tokens + sq.start + k0 + threadIdx.x] = w;
+  }
+}
+
+template <typename K>
+cudaError_t launch_sized(K kernel, size_t smem, int64_t tiles, const PromptParams& p, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3((unsigned)tiles), dim3(kThreads), smem, s, p);
+}
+
+template <typename T>
+cudaError_t launch_attention_t(const PromptParams& p, int64_t tiles, cudaStream_t s) {
+  auto smem = [](int nc) {
+    return ((size_t)(kPromptRows + kPromptKeys) * (64 * nc + 4) + kPromptRows * kPStride) * sizeof(float);
+  };
+  if (p.D <= 64) return launch_sized(prompt_simt_kernel<T, 1>, smem(1), tiles, p, s);
+  if (p.D <= 128) return launch_sized(prompt_simt_kernel<T, 2>, smem(2), tiles, p, s);
+  return launch_sized(prompt_simt_kernel<T, 4>, smem(4), tiles, p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s) {
+  return dtype == 0 ? launch_attention_t<__nv_bfloat16>(p, tiles, s) : launch_attention_t<float>(p, tiles, s);
+}
+
+cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s) {
+  const size_t smem = ((size_t)(kPromptRows + kPromptKeys) * (p.D + 4) + 16 * 64) * sizeof(float);
+  return dtype == 0 ? launch_sized(weights_simt_kernel<__nv_bfloat16>, smem, tiles, p, s)
+                    : launch_sized(weights_simt_kernel<float>, smem, tiles, p, s);
+}
+
+}  // namespace kvq
