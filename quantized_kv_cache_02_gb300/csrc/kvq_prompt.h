@@ -3,6 +3,8 @@
 // a launch takes its tiles, and the launchers.
 #pragma once
 
+#include <cuda.h>
+
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -84,6 +86,16 @@ struct EvictParams {
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
 cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s);
+
+// the tensor-core attention (bf16, head_dim 64 or 128); a tile of its order is
+// prompt_tc_tokens(g) tokens
+cudaError_t launch_prompt_tc(const PromptParams& p, int64_t tiles, cudaStream_t s);
+int prompt_tc_tokens(int g);
+
+// TMA map of a bf16 tensor (channel, d1, d2) with strides s1, s2 (elements) and
+// boxes of 64 channels x b1 x b2, 128-byte swizzled; false if the driver refuses it.
+bool tma_map3(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1,
+              int b2);
 
 // Rows of a CUDA-core attention tile and keys of one of its steps.
 constexpr int kPromptRows = 64, kPromptKeys = 64;

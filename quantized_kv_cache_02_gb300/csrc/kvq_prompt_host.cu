@@ -14,6 +14,34 @@
 #include "kvq_host.h"
 #include "kvq_prompt.h"
 
+namespace kvq {
+
+bool tma_map3(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1,
+              int b2) {
+  // the driver's encoder, looked up once (the library does not link libcuda)
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<Encode>(fn);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+  // the stride of a dimension of one entry is not used: any legal one
+  const cuuint64_t strides[2] = {(cuuint64_t)(d1 > 1 ? s1 : d0) * 2, (cuuint64_t)(d2 > 1 ? s2 : d0) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2}, step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace kvq
+
 namespace {
 
 using kvq::cuda_fail;
@@ -167,14 +195,16 @@ kvq_status prompt_attention(const kvq_prompt* p, const void* q, const void* k, c
   pp.v = v;
   pp.out = out;
   pp.lse = lse;
-  const int step = kvq::kPromptRows / pp.g;
+  const bool tc = p->dtype == KVQ_BF16 && (p->head_dim == 64 || p->head_dim == 128);
+  const int step = tc ? kvq::prompt_tc_tokens(pp.g) : kvq::kPromptRows / pp.g;
   const auto launches = launches_of(p);
   for (const auto& l : launches)
     if (fill_tiles(l, pp.Hkv, step, &pp.tiles) > kMaxTiles) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
   for (const auto& l : launches) {
     const int64_t tiles = fill_tiles(l, pp.Hkv, step, &pp.tiles);
-    const cudaError_t e =
-        kvq::launch_prompt_simt(pp, p->dtype == KVQ_BF16 ? 0 : 1, tiles, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = tc ? kvq::launch_prompt_tc(pp, tiles, s)
+                             : kvq::launch_prompt_simt(pp, p->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
     if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
     kvq::count_launches(1);
   }

@@ -1,0 +1,358 @@
+// Prompt attention on the fifth-generation tensor cores: bf16, head_dim 64 or
+// 128 (kvq_prompt_attention).
+//
+// A row is a (token, query head) pair of one KV head, token major: the heads
+// that share a KV head share its Key and Value tiles and the causal boundary.
+// A CTA holds two tiles of 128 rows (floor(128 / g) tokens each) and walks the
+// keys in blocks of 128, both tiles on the same Key and Value tile:
+//
+//   S_i = Q_i K^T       128 x 128, fp32 in tensor memory (Q, K from shared memory)
+//   P_i = 2^(S_i c - m) bf16, over S_i in tensor memory
+//   O_i += P_i V        128 x d, fp32 in tensor memory (P from tensor memory)
+//
+// Warps 0-3 and 4-7 run the softmax of tile 0 and 1, one row a thread, so
+// maxima and sums need no exchange; warp 8 issues the MMAs, warp 9 the TMA
+// copies.  The tiles alternate: one tile's MMAs run under the other's softmax.
+// The running maximum moves only when a score passes it by 2^8 (a row's sums
+// stay exact in fp32 either way), so O is rescaled rarely and by the softmax
+// threads themselves.
+// ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d) + M) V.)
+
+#include "kvq_prompt.h"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kTcThreads = 384;  // warps 10 and 11 only fill the third warpgroup
+// Registers a thread after the split of the launch's 3 x 168: a softmax thread
+// holds a whole row of scores.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr float kSlack = 8.f;
+
+// A wait that every lane of the warp leaves with the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+}
+
+template <int D>
+struct TcLayout {
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t kChunk = 128 * 128;           // 128 rows of 64 channels
+  static constexpr uint32_t kTile = kChunk * (D / 64);    // a Q, K or V tile
+  static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile;
+  // barriers: full / empty per stage, then per tile: Q, S, P, PV
+  static constexpr int kNBars = 2 * kStages + 8;
+  static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;  // + alignment
+  static constexpr uint32_t kColS = 0, kColO = 256;       // S_i at 128 i, O_i at 256 + D i
+};
+
+struct TcMaps {
+  CUtensorMap q, k, v;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ TcMaps maps) {
+  using L = TcLayout<D>;
+  extern __shared__ uint8_t tc_raw[];
+  uint8_t* smem = tc_raw + ((1024u - (smem_u32(tc_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kStages;
+  const uint32_t bar_q = bar_empty + 8 * L::kStages, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_pv = bar_p + 16;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+
+  int si, h, level;
+  prompt_tile(p.tiles, blockIdx.x, &si, &h, &level);
+  const PromptSeq sq = p.tiles.seq[si];
+  const int tile_tok = p.tiles.step / 2;            // tokens of a tile
+  const int tok0 = level * p.tiles.step;            // of tile 0
+  // key blocks of each tile: through its last token
+  const int end0 = min(sq.len, tok0 + tile_tok), end1 = min(sq.len, tok0 + 2 * tile_tok);
+  const int n0 = (end0 + kKeys - 1) / kKeys, n1 = tok0 + tile_tok < sq.len ? (end1 + kKeys - 1) / kKeys : 0;
+  const int nmax = max(n0, n1);
+
+  if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
+  if (t == 0) {
+    *abort = 0;
+    for (int s = 0; s < L::kStages; ++s) {
+      bar_init(bar_full + 8 * s, 1);
+      bar_init(bar_empty + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar_q + 8 * i, 1);
+      bar_init(bar_s + 8 * i, 1);
+      bar_init(bar_p + 8 * i, 128);
+      bar_init(bar_pv + 8 * i, 1);
+    }
+    bar_init_fence();
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *tslot;
+  pdl_wait();
+  pdl_release();
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+      // ============ copies: Q0, K0, Q1, then V_j, K_j+1 ==============================
+      if (lane == 0) {
+        tma_prefetch(&maps.q);
+        tma_prefetch(&maps.k);
+        tma_prefetch(&maps.v);
+        const uint32_t qbytes = (uint32_t)(tile_tok * p.g) * 128u * (D / 64);
+        auto load_q = [&](int i) {
+          bar_expect(bar_q + 8 * i, qbytes);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load3(sbase + L::kQ + i * L::kTile + c * L::kChunk, &maps.q, 64 * c, h * p.g,
+                      sq.start + tok0 + i * tile_tok, bar_q + 8 * i);
+        };
+        int issued = 0;
+        auto load_kv = [&](const CUtensorMap* m, int blk) -> bool {
+          const int s = issued % L::kStages, round = issued / L::kStages;
+          if (round > 0 && !bar_wait(bar_empty + 8 * s, (uint32_t)(round - 1) & 1u, abort)) return false;
+          bar_expect(bar_full + 8 * s, L::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load3(sbase + L::kRing + s * L::kTile + c * L::kChunk, m, 64 * c, sq.start + blk * kKeys, h,
+                      bar_full + 8 * s);
+          ++issued;
+          return true;
+        };
+        load_q(0);
+        bool go = load_kv(&maps.k, 0);
+        if (n1 > 0) load_q(1);
+        for (int j = 0; go && j < nmax; ++j) {
+          go = load_kv(&maps.v, j);
+          if (go && j + 1 < nmax) go = load_kv(&maps.k, j + 1);
+        }
+        if (!go) *abort = 1;
+        // nothing in flight when the CTA ends (all have landed long since, unless it stops early)
+        for (int x = max(0, issued - L::kStages); x < issued; ++x)
+          bar_drain(bar_full + 8 * (x % L::kStages), (uint32_t)(x / L::kStages) & 1u);
+        bar_drain(bar_q, 0);
+        if (n1 > 0) bar_drain(bar_q + 8, 0);
+      }
+    } else if (warp == kMmaWarp) {
+      // ============ MMAs (lane 0; the other lanes help clear Value rows) =============
+      constexpr uint32_t idesc_s = bf16_idesc(kRows, kKeys, false), idesc_o = bf16_idesc(kRows, D, true);
+      int taken = 0;  // ring tiles waited for
+      auto next_tile = [&](uint32_t* addr) -> bool {
+        const int s = taken % L::kStages;
+        const bool ok = warp_wait(bar_full + 8 * s, (uint32_t)(taken / L::kStages) & 1u, abort);
+        *addr = sbase + L::kRing + s * L::kTile;
+        ++taken;
+        return ok;
+      };
+      auto scores = [&](int i, uint32_t kaddr) {
+        const uint64_t a = sw128_desc(sbase + L::kQ + i * L::kTile, 0), b = sw128_desc(kaddr, 0);
+  #pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
+          mma_ss(tm + L::kColS + 128 * i, a + off, b + off, idesc_s, ks > 0);
+        }
+        mma_commit(bar_s + 8 * i);
+      };
+      bool ok = true;
+      uint32_t kaddr = 0, vaddr = 0;
+      ok = next_tile(&kaddr);
+      for (int i = 0; i < 2 && ok; ++i) {
+        if (i == 1 && n1 == 0) break;
+        ok = warp_wait(bar_q + 8 * i, 0, abort);
+        tm_fence_after();
+        if (ok && lane == 0) scores(i, kaddr);
+      }
+      if (lane == 0) mma_commit(bar_empty + 8 * ((taken - 1) % L::kStages));
+      int pv[2] = {0, 0};
+      for (int j = 0; j < nmax && ok; ++j) {
+        ok = next_tile(&vaddr);
+        if (!ok) break;
+        const int vstage = (taken - 1) % L::kStages;
+        // rows of the block past the sequence hold other sequences' values: a
+        // weight of 0 does not silence a NaN there, so what a k-step of 16 covers is cleared
+        const int valid = sq.len - j * kKeys;
+        if (valid < kKeys && (valid & 15)) {
+          const int r1 = (valid + 15) & ~15;
+          for (int x = lane; x < (r1 - valid) * 8 * (D / 64); x += 32) {
+            const int c = x / ((r1 - valid) * 8), y = x - c * (r1 - valid) * 8;
+            *reinterpret_cast<uint4*>(smem + (vaddr - sbase) + c * L::kChunk + (valid + y / 8) * 128 + (y & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          async_proxy_fence();
+          __syncwarp();
+        }
+        const bool more = j + 1 < nmax;
+        if (more) ok = next_tile(&kaddr);
+        if (!ok) break;
+        for (int i = 0; i < 2; ++i) {
+          const int ni = i ? n1 : n0;
+          if (j < ni) {
+            if (!(ok = warp_wait(bar_p + 8 * i, (uint32_t)j & 1u, abort))) break;
+            tm_fence_after();
+            const int steps = min(8, (min(i ? end1 : end0, sq.len) - j * kKeys + 15) / 16);
+            if (lane == 0) {
+              const uint64_t b = sw128_desc(vaddr, L::kChunk);
+              for (int ks = 0; ks < steps; ++ks)
+                mma_ts(tm + L::kColO + D * i, tm + L::kColS + 128 * i + 8 * ks, b + ks * (2048 >> 4), idesc_o,
+                       j > 0 || ks > 0);
+              mma_commit(bar_pv + 8 * i);
+            }
+            ++pv[i];
+            if (j + 1 < ni) {
+              // S_i and P_i share their columns: the output MMAs have read P_i
+              if (!(ok = warp_wait(bar_pv + 8 * i, (uint32_t)j & 1u, abort))) break;
+              if (lane == 0) scores(i, kaddr);
+            }
+          }
+        }
+        if (lane == 0) {
+          mma_commit(bar_empty + 8 * vstage);
+          if (more) mma_commit(bar_empty + 8 * ((taken - 1) % L::kStages));
+        }
+        __syncwarp();
+      }
+      if (!ok) *abort = 1;
+      // nothing in flight when the CTA ends
+      for (int i = 0; i < 2; ++i)
+        if (pv[i] > 0) bar_drain(bar_pv + 8 * i, (uint32_t)(pv[i] - 1) & 1u);
+      if (!ok && lane == 0) {
+        mma_commit(bar_q);  // its one phase is over: a second one for this
+        bar_drain(bar_q, 1);
+      }
+    }
+  } else {
+    // ============ softmax: tile i, one row a thread ===================================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int i = warp >> 2, r = t & 127;
+    const int n = i ? n1 : n0;
+    const int tt = r / p.g, pos = tok0 + i * tile_tok + tt;
+    const bool live = tt < tile_tok && pos < sq.len;
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tm + L::kColS + 128 * i + lanes, to = tm + L::kColO + D * i + lanes;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = warp_wait(bar_s + 8 * i, (uint32_t)j & 1u, abort))) break;
+      if (warp_live) {
+        tm_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tm_ld32(ts + 32 * c, s + 32 * c);
+        tm_wait_ld();
+        const int limit = pos - j * kKeys;  // the last key of the block this row sees
+        if (__any_sync(0xffffffffu, limit < kKeys - 1)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > limit) s[c] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 128; c += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
+        const bool up = top > m + kSlack;
+        if (__any_sync(0xffffffffu, up)) {
+          const float a = up ? ex2(m - top) : 1.f;
+          if (up) m = top;
+          l *= a;
+          if (j > 0) {
+            if (!(ok = warp_wait(bar_pv + 8 * i, (uint32_t)(j - 1) & 1u, abort))) break;
+            tm_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tm_ld32(to + 32 * c, o);
+              tm_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= a;
+              tm_st32(to + 32 * c, o);
+            }
+          }
+        }
+        const float2 sc = make_float2(p.scale2, p.scale2), nm = make_float2(-m, -m);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float2 x = fma2(make_float2(s[c + e], s[c + e + 1]), sc, nm);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
+            w[e / 2] = pack_bf16(x.x, x.y);
+          }
+          tm_st16(ts + c / 2, w);
+        }
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+        tm_wait_st();
+        tm_fence_before();
+      }
+      bar_arrive(bar_p + 8 * i);
+    }
+    if (ok && n > 0) ok = warp_wait(bar_pv + 8 * i, (uint32_t)(n - 1) & 1u, abort);
+    if (!ok) {
+      *abort = 1;
+      if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
+    } else if (n > 0 && warp_live) {
+      tm_fence_after();
+      const float inv = 1.f / l;
+      const int head = h * p.g + r - tt * p.g;
+      __nv_bfloat16* dst =
+          static_cast<__nv_bfloat16*>(p.out) + (int64_t)(sq.start + pos) * p.o_ts + (int64_t)head * p.o_hs;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tm_ld32(to + 32 * c, o);
+        tm_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(dst + 32 * c + e) =
+                make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                           pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+        }
+      }
+      if (live && p.lse)
+        p.lse[(int64_t)head * p.n_tokens + sq.start + pos] = (m + log2f(l)) * 0.69314718055994530942f;
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tm_free<512>(tm);
+  }
+}
+
+template <int D>
+cudaError_t launch_tc(const PromptParams& p, const TcMaps& maps, int64_t tiles, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)TcLayout<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prompt_tc_kernel<D>, dim3((unsigned)tiles), dim3(kTcThreads), TcLayout<D>::kSmem, s, p, maps);
+}
+
+}  // namespace
+
+int prompt_tc_tokens(int g) { return 2 * (kRows / g); }
+
+cudaError_t launch_prompt_tc(const PromptParams& p, int64_t tiles, cudaStream_t s) {
+  TcMaps maps;
+  // dims (channel, head, token) for the queries, (channel, token, head) for Keys and Values
+  if (!tma_map3(&maps.q, p.q, p.D, p.Hq, p.n_tokens, p.q_hs, p.q_ts, p.g, kRows / p.g) ||
+      !tma_map3(&maps.k, p.k, p.D, p.n_tokens, p.Hkv, p.k_ts, p.k_hs, kKeys, 1) ||
+      !tma_map3(&maps.v, p.v, p.D, p.n_tokens, p.Hkv, p.v_ts, p.v_hs, kKeys, 1))
+    return cudaErrorInvalidValue;
+  return p.D == 128 ? launch_tc<128>(p, maps, tiles, s) : launch_tc<64>(p, maps, tiles, s);
+}
+
+}  // namespace kvq
