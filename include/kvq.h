@@ -180,7 +180,7 @@ typedef struct kvq_prompt {
   int32_t head_dim;     /* d: a multiple of 16, 16 <= d <= 256 */
   int32_t dtype;        /* kvq_dtype of q, k, v, out and the kept rows */
   const int64_t* seq_lens; /* host array of n_seqs lengths, read during the call */
-  int64_t n_tokens;     /* token rows the tensors have (>= the lengths' sum, < 2^31) */
+  int64_t n_tokens;     /* token rows the tensors have (>= the lengths' sum, <= 2^30) */
   int64_t q_token_stride, q_head_stride;
   int64_t k_token_stride, k_head_stride;
   int64_t v_token_stride, v_head_stride;

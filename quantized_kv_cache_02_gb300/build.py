@@ -24,7 +24,8 @@ LDFLAGS = ARCH + ["-shared", "-cudart", "shared", f"-Xlinker=-rpath={CUDA_HOME}/
 
 SOURCES = ["kvq_host.cu", "kvq_append.cu", "kvq_decode_simt.cu", "kvq_decode_mma.cu", "kvq_decode_mma_b2.cu",
            "kvq_decode_mma_b4.cu", "kvq_decode_mma_b8.cu", "kvq_decode_tc.cu", "kvq_restore.cu",
-           "kvq_segment.cu", "kvq_prompt_host.cu", "kvq_prompt_simt.cu", "kvq_prompt_tc.cu", "kvq_evict.cu"]
+           "kvq_segment.cu", "kvq_prompt_host.cu", "kvq_prompt_simt.cu", "kvq_prompt_tc.cu", "kvq_weights_tc.cu",
+           "kvq_evict.cu"]
 
 
 def _run(cmd):

@@ -58,6 +58,8 @@ struct PromptParams {
   float* weights;              // [Hkv][n_tokens]
   int64_t n_tokens;
   int64_t last;                // weights: queries counted back from each sequence's end
+  float lse_hi, lse_lo;        // weights: sqrt(D) * scale2 as two floats, lse times it is in the scores' units
+  int32_t split;               // weights on the tensor cores: CTAs that share a pair of key tiles
   int32_t* status;
   PromptTiles tiles;
 };
@@ -91,6 +93,12 @@ cudaError_t launch_evict(const EvictParams& p, int32_t max_len, int32_t max_keep
 // prompt_tc_tokens(g) tokens
 cudaError_t launch_prompt_tc(const PromptParams& p, int64_t tiles, cudaStream_t s);
 int prompt_tc_tokens(int g);
+
+// the tensor-core weights: ``pairs`` pairs of 128-key tiles (KV heads counted)
+// and at most most_tokens counted tokens a sequence; a CTA takes ``chunk``
+// pairs, or a cluster of ``split`` CTAs one pair
+void weights_tc_plan(int64_t pairs, int64_t most_tokens, int g, int n_sm, int* chunk, int* split);
+cudaError_t launch_weights_tc(const PromptParams& p, int64_t tiles, cudaStream_t s);
 
 // TMA map of a bf16 tensor (channel, d1, d2) with strides s1, s2 (elements) and
 // boxes of 64 channels x b1 x b2, 128-byte swizzled; false if the driver refuses it.

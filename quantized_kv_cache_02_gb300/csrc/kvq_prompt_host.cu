@@ -47,6 +47,7 @@ namespace {
 using kvq::cuda_fail;
 using kvq::fail;
 
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // positions and tile ends stay within 32 bits
 constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
 
 int esize_of(const kvq_prompt* p) { return p->dtype == KVQ_BF16 ? 2 : 4; }
@@ -66,8 +67,8 @@ kvq_status check_prompt(const kvq_prompt* p, int64_t* total) {
     return fail(KVQ_EUNSUPPORTED, "head_dim must be a multiple of 16 in [16, 256] (got %d)", p->head_dim);
   if (p->dtype != KVQ_BF16 && p->dtype != KVQ_FP32) return fail(KVQ_EINVAL, "unknown dtype %d", p->dtype);
   if (!p->seq_lens) return fail(KVQ_EINVAL, "seq_lens is NULL");
-  if (p->n_tokens < 0 || p->n_tokens >= (int64_t(1) << 31))
-    return fail(KVQ_EINVAL, "n_tokens must be in [0, 2^31) (got %lld)", (long long)p->n_tokens);
+  if (p->n_tokens < 0 || p->n_tokens > kMaxTokens)
+    return fail(KVQ_EINVAL, "n_tokens must be in [0, 2^30] (got %lld)", (long long)p->n_tokens);
   int64_t sum = 0;
   for (int i = 0; i < p->n_seqs; ++i) {
     if (p->seq_lens[i] < 0 || p->seq_lens[i] > p->n_tokens - sum)
@@ -138,6 +139,18 @@ std::vector<std::vector<kvq::PromptSeq>> launches_of(const kvq_prompt* p) {
   return out;
 }
 
+// The tensor-core kernels' shapes.
+bool tensor_cores(const kvq_prompt* p) {
+  return p->dtype == KVQ_BF16 && (p->head_dim == 64 || p->head_dim == 128);
+}
+
+kvq_status sm_count(int* n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "cudaDeviceGetAttribute");
+}
+
 // Tiles of ``step`` tokens over the sequences; returns their number.
 int64_t fill_tiles(const std::vector<kvq::PromptSeq>& seqs, int hkv, int step, kvq::PromptTiles* t) {
   t->n_seqs = (int32_t)seqs.size();
@@ -195,7 +208,7 @@ kvq_status prompt_attention(const kvq_prompt* p, const void* q, const void* k, c
   pp.v = v;
   pp.out = out;
   pp.lse = lse;
-  const bool tc = p->dtype == KVQ_BF16 && (p->head_dim == 64 || p->head_dim == 128);
+  const bool tc = tensor_cores(p);
   const int step = tc ? kvq::prompt_tc_tokens(pp.g) : kvq::kPromptRows / pp.g;
   const auto launches = launches_of(p);
   for (const auto& l : launches)
@@ -231,14 +244,31 @@ kvq_status prompt_weights(const kvq_prompt* p, const void* q, const void* k, con
   pp.lse = const_cast<float*>(lse);
   pp.weights = weights;
   pp.last = last;
+  // sqrt(d) times the rounded factor of the scores (scale2), as two floats
+  const double r = std::sqrt((double)pp.D) * (double)pp.scale2;
+  pp.lse_hi = (float)r;
+  pp.lse_lo = (float)(r - (double)pp.lse_hi);
+  pp.split = 1;
+  const bool tc = tensor_cores(p);
+  int n_sm = 0;
+  if (tc) KVQ_TRY(sm_count(&n_sm));
   const auto launches = launches_of(p);
+  auto step_of = [&](const std::vector<kvq::PromptSeq>& l) {
+    if (!tc) return kvq::kPromptKeys;
+    int64_t pairs = 0;
+    for (const kvq::PromptSeq& q1 : l) pairs += (int64_t)kvq::prompt_blocks(q1.len, 256) * pp.Hkv;
+    int chunk;
+    kvq::weights_tc_plan(pairs, std::min<int64_t>(last, l[0].len), pp.g, n_sm, &chunk, &pp.split);
+    return 256 * chunk;
+  };
   for (const auto& l : launches)
-    if (fill_tiles(l, pp.Hkv, kvq::kPromptKeys, &pp.tiles) > kMaxTiles)
+    if (fill_tiles(l, pp.Hkv, step_of(l), &pp.tiles) * pp.split > kMaxTiles)
       return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
   for (const auto& l : launches) {
-    const int64_t tiles = fill_tiles(l, pp.Hkv, kvq::kPromptKeys, &pp.tiles);
-    const cudaError_t e =
-        kvq::launch_weights_simt(pp, p->dtype == KVQ_BF16 ? 0 : 1, tiles, static_cast<cudaStream_t>(stream));
+    const int64_t tiles = fill_tiles(l, pp.Hkv, step_of(l), &pp.tiles);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = tc ? kvq::launch_weights_tc(pp, tiles, s)
+                             : kvq::launch_weights_simt(pp, p->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
     if (e != cudaSuccess) return cuda_fail(e, "prompt weights launch");
     kvq::count_launches(1);
   }

@@ -31,11 +31,6 @@ constexpr int kMmaWarp = 8, kCopyWarp = 9, kTcThreads = 384;  // warps 10 and 11
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr float kSlack = 8.f;
 
-// A wait that every lane of the warp leaves with the same answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
-}
-
 template <int D>
 struct TcLayout {
   static constexpr int kStages = D == 128 ? 5 : 8;

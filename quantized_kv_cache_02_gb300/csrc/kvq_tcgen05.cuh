@@ -43,7 +43,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const vo
   }
   return false;
 }
-// The same, not cut short: for copies and MMAs in flight when a CTA stops.
+// A wait that every lane of the warp leaves with the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+}
+// A wait that is not cut short: for copies and MMAs in flight when a CTA stops.
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
   for (uint32_t it = 0; it < kBarTries; ++it)
     if (bar_try(bar, parity)) return;

@@ -1,0 +1,357 @@
+// Gathered prompt weights on the fifth-generation tensor cores: bf16, head_dim
+// 64 or 128 (kvq_prompt_weights).
+//
+//   w_j = sum over the counted rows r of 2^(s_jr - L_r),  s_jr = k_j . q_r log2(e) / sqrt(d)
+//
+// A row r is a (token, query head) pair of the KV head, token major; a query
+// tile is 128 rows (floor(128 / g) tokens).  Keys are the M side of the MMA,
+//
+//   S^T = K Q^T    128 keys x 128 rows, fp32 in tensor memory,
+//
+// so a thread owns one key and its sum never leaves a register.  A CTA takes
+// pairs of key tiles: warps 0-3 sum the first, warps 4-7 the second, and both
+// use every query tile that arrives.  Each key tile has two score buffers, so
+// MMAs and exponentials overlap.  With few counted queries (at most two tiles)
+// the query tiles stay in shared memory and a run of pairs streams past them;
+// else a CTA has one pair, which stays while the queries stream.
+// ``split`` CTAs of a cluster take a pair's query tiles in turn and rank 0 adds
+// their sums in rank order, so a short prompt fills the GPU and the result
+// has the same bits every time.
+//
+// Exponent: with the rounded factor c ~ log2(e) / sqrt(d), s c - L and
+// L = lse sqrt(d) c differ from the exact exponent only by a factor 1 + 2^-24
+// on what is near 0 where a weight counts.  L is kept as a float and the
+// remainder enters as the factor 2^-rest on the row's terms (one fused
+// multiply-add in place of the sum's addition).
+// ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d) + M).)
+
+#include <algorithm>
+
+#include "kvq_prompt.h"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kKeys = 128, kRows = 128;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kWThreads = 384;  // warps 10 and 11 only fill the third warpgroup
+constexpr int kSumRegs = 200, kOtherRegs = 104;              // a thread, out of the launch's 3 x 168
+constexpr int kQStages = 4, kStayTiles = 2;
+
+template <int D>
+struct WLayout {
+  static constexpr uint32_t kChunk = 128 * 128;
+  static constexpr uint32_t kTile = kChunk * (D / 64);
+  // what streams, and what stays: two key pairs past two query tiles, or four query tiles past one key pair
+  static constexpr uint32_t kStream = 0, kStay = 4 * kTile;
+  static constexpr uint32_t kL = kStay + 2 * kTile;              // per query tile 64 x {L0, L1, f0, f1}
+  static constexpr uint32_t kRed = kL + kQStages * 1024;           // [8 ranks][256 keys]
+  static constexpr uint32_t kBars = kRed + 8 * 256 * 4;
+  // K full / empty (2 each), Q full / empty, S full / empty (tile, buffer)
+  static constexpr int kNBars = 4 + 2 * kQStages + 8;
+  static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;
+};
+
+struct WMaps {
+  CUtensorMap q, k;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWThreads, 1)
+    weights_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ WMaps maps) {
+  using L = WLayout<D>;
+  extern __shared__ uint8_t w_raw[];
+  uint8_t* smem = w_raw + ((1024u - (smem_u32(w_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t bar_kf = sbase + L::kBars, bar_ke = bar_kf + 16, bar_qf = bar_ke + 16,
+                 bar_qe = bar_qf + 8 * kQStages, bar_sf = bar_qe + 8 * kQStages, bar_se = bar_sf + 32;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+
+  int si, h, level;
+  const int rank = blockIdx.x % p.split;  // clusters are ``split`` CTAs in a row
+  prompt_tile(p.tiles, blockIdx.x / p.split, &si, &h, &level);
+  const PromptSeq sq = p.tiles.seq[si];
+  const int run0 = (prompt_blocks(sq.len, p.tiles.step) - 1 - level) * p.tiles.step;  // first key
+  const int pairs = min(p.tiles.step / (2 * kKeys), (sq.len - run0 + 2 * kKeys - 1) / (2 * kKeys));
+  const int tile_tok = kRows / p.g;
+  const int tok0 = (int)max((int64_t)0, sq.len - p.last);  // first counted token
+  const int nq = (sq.len - tok0 + tile_tok - 1) / tile_tok;
+  const bool resident = p.split == 1 && nq <= kStayTiles;
+  auto k_tile = [&](int pr, int w) { return (resident ? L::kStream + 2 * (pr & 1) * L::kTile : L::kStay) + w * L::kTile; };
+  auto q_tile = [&](int s) { return (resident ? L::kStay : L::kStream) + s * L::kTile; };
+  // the first query tile that sees a key of the pair; this CTA takes every split-th from there
+  auto q_first = [&](int pair) {
+    const int key = run0 + pair * 2 * kKeys;
+    return (resident || key < tok0 ? 0 : (key - tok0) / tile_tok) + rank;
+  };
+
+  if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
+  if (t == 0) {
+    *abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar_kf + 8 * i, 1);
+      bar_init(bar_ke + 8 * i, 1);
+    }
+    for (int i = 0; i < kQStages; ++i) {
+      bar_init(bar_qf + 8 * i, 1 + 32);  // the copy, and the lanes that wrote L
+      bar_init(bar_qe + 8 * i, 1 + 8);   // the MMAs, and the summing warps
+    }
+    for (int i = 0; i < 4; ++i) {
+      bar_init(bar_sf + 8 * i, 1);
+      bar_init(bar_se + 8 * i, 128);
+    }
+    bar_init_fence();
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *tslot;
+  if (p.split > 1)  // a rank's shared memory is written to only once it runs
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  pdl_wait();
+  pdl_release();
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+      // ============ copies; the lanes turn lse into L =================================
+      if (lane == 0) {
+        tma_prefetch(&maps.q);
+        tma_prefetch(&maps.k);
+      }
+      const uint32_t qbytes = (uint32_t)(tile_tok * p.g) * 128u * (D / 64);
+      auto row_lse = [&](int i, int r) -> float {
+        const int tt = r / p.g, pos = tok0 + i * tile_tok + tt;
+        return tt < tile_tok && pos < sq.len
+                   ? p.lse[(int64_t)(h * p.g + r - tt * p.g) * p.n_tokens + sq.start + pos]
+                   : 0.f;
+      };
+      float ahead[4];
+      int ahead_tile = -1;
+      auto fetch_lse = [&](int i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ahead[e] = row_lse(i, 32 * e + lane);
+        ahead_tile = i;
+      };
+      int issued = 0, kpairs = 0;
+      bool go = true;
+      auto load_q = [&](int i, int then) {  // tile i; its successor's lse is fetched under it
+        const int s = issued % kQStages, round = issued / kQStages;
+        if (ahead_tile != i) fetch_lse(i);
+        float now[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) now[e] = ahead[e];
+        if (then >= 0) fetch_lse(then);
+        if (round > 0 && !(go = warp_wait(bar_qe + 8 * s, (uint32_t)(round - 1) & 1u, abort))) return;
+        if (lane == 0) {
+          bar_expect(bar_qf + 8 * s, qbytes);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load3(sbase + q_tile(s) + c * L::kChunk, &maps.q, 64 * c, h * p.g,
+                      sq.start + tok0 + i * tile_tok, bar_qf + 8 * s);
+        }
+        float* dst = reinterpret_cast<float*>(smem + L::kL + s * 1024);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 32 * e + lane;
+          const float hi = __fmul_rn(now[e], p.lse_hi), rest = fmaf(now[e], p.lse_hi, -hi) + now[e] * p.lse_lo;
+          dst[(r >> 1) * 4 + (r & 1)] = hi;
+          dst[(r >> 1) * 4 + 2 + (r & 1)] = ex2(-rest);
+        }
+        bar_arrive(bar_qf + 8 * s);
+        ++issued;
+      };
+      for (int pr = 0; pr < pairs && go; ++pr) {
+        const int s = pr & 1;
+        if (pr > 1 && !(go = warp_wait(bar_ke + 8 * s, (uint32_t)(pr / 2 - 1) & 1u, abort))) break;
+        const int key = run0 + pr * 2 * kKeys, both = key + kKeys < sq.len;
+        if (lane == 0) {
+          bar_expect(bar_kf + 8 * s, L::kTile * (both ? 2 : 1));
+          for (int w = 0; w < 1 + both; ++w)
+            for (int c = 0; c < D / 64; ++c)
+              tma_load3(sbase + k_tile(pr, w) + c * L::kChunk, &maps.k, 64 * c,
+                        sq.start + key + w * kKeys, h, bar_kf + 8 * s);
+        }
+        ++kpairs;
+        if (pr == 0 || !resident)
+          for (int i = q_first(pr); i < nq && go; i += p.split) load_q(i, i + p.split < nq ? i + p.split : -1);
+      }
+      if (!go) *abort = 1;
+      // nothing in flight when the CTA ends
+      for (int x = max(0, kpairs - 2); x < kpairs; ++x) bar_drain(bar_kf + 8 * (x & 1), (uint32_t)(x / 2) & 1u);
+      for (int x = max(0, issued - kQStages); x < issued; ++x)
+        bar_drain(bar_qf + 8 * (x % kQStages), (uint32_t)(x / kQStages) & 1u);
+    } else if (warp == kMmaWarp) {
+      // ============ MMAs (lane 0) =======================================================
+      constexpr uint32_t idesc = bf16_idesc(kKeys, kRows, false);
+      int taken = 0, n_s[2] = {0, 0};
+      bool ok = true;
+      for (int pr = 0; pr < pairs && ok; ++pr) {
+        const int both = run0 + pr * 2 * kKeys + kKeys < sq.len;
+        ok = warp_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort);
+        for (int i = q_first(pr); i < nq && ok; i += p.split) {
+          const int s = resident ? i : taken % kQStages;
+          ok = warp_wait(bar_qf + 8 * s, resident ? 0u : (uint32_t)(taken / kQStages) & 1u, abort);
+          ++taken;
+          for (int w = 0; w < 1 + both && ok; ++w) {
+            const int b = 2 * w + (n_s[w] & 1);
+            if (n_s[w] > 1) ok = warp_wait(bar_se + 8 * b, (uint32_t)(n_s[w] / 2 - 1) & 1u, abort);
+            if (!ok) break;
+            tm_fence_after();
+            if (lane == 0) {
+              const uint64_t da = sw128_desc(sbase + k_tile(pr, w), 0);
+              const uint64_t db = sw128_desc(sbase + q_tile(s), 0);
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
+                mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > 0);
+              }
+              mma_commit(bar_sf + 8 * b);
+            }
+            ++n_s[w];
+          }
+          if (lane == 0 && !resident) mma_commit(bar_qe + 8 * s);
+        }
+        if (lane == 0) mma_commit(bar_ke + 8 * (pr & 1));
+        __syncwarp();
+      }
+      if (!ok) *abort = 1;
+      // nothing in flight when the CTA ends: the last commit on a score buffer covers the MMAs before it
+      for (int w = 0; w < 2; ++w)
+        for (int x = max(0, n_s[w] - 2); x < n_s[w]; ++x) bar_drain(bar_sf + 8 * (2 * w + (x & 1)), (uint32_t)(x / 2) & 1u);
+    }
+  } else {
+    // ============ sums: key tile w, one key a thread ==================================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    const int w = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const float2 sc = make_float2(p.scale2, p.scale2);
+    int taken = 0, n_s = 0;
+    bool ok = true;
+    for (int pr = 0; pr < pairs && ok; ++pr) {
+      const int tile_key = run0 + pr * 2 * kKeys + w * kKeys, key = tile_key + (t & 127);
+      const bool active = tile_key < sq.len;
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      for (int i = q_first(pr); i < nq && ok; i += p.split) {
+        const int s = resident ? i : taken % kQStages;
+        const uint32_t qpar = resident ? 0u : (uint32_t)(taken / kQStages) & 1u;
+        ++taken;
+        if (active) {
+          const int b = 2 * w + (n_s & 1);
+          ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n_s / 2) & 1u, abort) && warp_wait(bar_qf + 8 * s, qpar, abort);
+          if (!ok) break;
+          ++n_s;
+          tm_fence_after();
+          // rows [lo, hi) of the tile count for this key
+          const int pos0 = tok0 + i * tile_tok;
+          const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
+          const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
+          const float4* lf = reinterpret_cast<const float4*>(smem + L::kL + s * 1024);
+          const uint32_t ts = tm + 128 * b + lanes;
+          float x[2][32];
+          tm_ld32(ts, x[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tm_wait_ld();
+            if (c < 3) tm_ld32(ts + 32 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float4 f = lf[16 * c + e / 2];
+              float2 y = fma2(make_float2(x[c & 1][e], x[c & 1][e + 1]), sc, make_float2(-f.x, -f.y));
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              if (masked) {
+                const int r = 32 * c + e;
+                y.x = r >= lo && r < hi ? y.x : 0.f;
+                y.y = r + 1 >= lo && r + 1 < hi ? y.y : 0.f;
+              }
+              sum[(e >> 1) & 1] = fma2(y, make_float2(f.z, f.w), sum[(e >> 1) & 1]);
+            }
+          }
+          tm_fence_before();
+          bar_arrive(bar_se + 8 * b);
+        }
+        if (!resident) {
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar_qe + 8 * s);
+        }
+      }
+      if (!ok) break;
+      sum[0] = add2(sum[0], sum[1]);
+      const float mine = sum[0].x + sum[0].y;
+      if (p.split > 1) {
+        // into rank 0's shared memory (one pair a CTA)
+        uint32_t dst = sbase + L::kRed + (uint32_t)(rank * 256 + t) * 4, remote;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(dst));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(mine) : "memory");
+      } else if (key < sq.len) {
+        p.weights[(int64_t)h * p.n_tokens + sq.start + key] = mine;
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tm_free<512>(tm);
+  }
+  if (p.split > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0 && t < 2 * kKeys && run0 + t < sq.len) {
+      const float* red = reinterpret_cast<const float*>(smem + L::kRed);
+      float sum = red[t];
+      for (int r = 1; r < p.split; ++r) sum += red[256 * r + t];
+      p.weights[(int64_t)h * p.n_tokens + sq.start + run0 + t] = sum;
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_w(const PromptParams& p, const WMaps& maps, int64_t tiles, cudaStream_t s) {
+  const size_t smem = WLayout<D>::kSmem;
+  const cudaError_t e =
+      cudaFuncSetAttribute(weights_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.split));
+  cfg.blockDim = dim3(kWThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, weights_tc_kernel<D>, p, maps);
+}
+
+}  // namespace
+
+void weights_tc_plan(int64_t pairs, int64_t most_tokens, int g, int n_sm, int* chunk, int* split) {
+  *chunk = *split = 1;
+  const int64_t tiles = (most_tokens + kRows / g - 1) / (kRows / g);  // query tiles of a pair, at most
+  if (tiles <= kStayTiles) {
+    *chunk = (int)std::min<int64_t>(1024, std::max<int64_t>(1, (pairs + n_sm - 1) / n_sm));
+  } else {
+    while (*split < 8 && pairs * *split < 2 * n_sm && tiles >= 8 * *split) *split *= 2;
+  }
+}
+
+cudaError_t launch_weights_tc(const PromptParams& p, int64_t tiles, cudaStream_t s) {
+  WMaps maps;
+  if (!tma_map3(&maps.q, p.q, p.D, p.Hq, p.n_tokens, p.q_hs, p.q_ts, p.g, kRows / p.g) ||
+      !tma_map3(&maps.k, p.k, p.D, p.n_tokens, p.Hkv, p.k_ts, p.k_hs, kKeys, 1))
+    return cudaErrorInvalidValue;
+  return p.D == 128 ? launch_w<128>(p, maps, tiles, s) : launch_w<64>(p, maps, tiles, s);
+}
+
+}  // namespace kvq

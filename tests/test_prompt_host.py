@@ -41,7 +41,7 @@ SHAPES = [(dict(n_seqs=0), B.KVQ_EINVAL), (dict(n_kv_heads=0), B.KVQ_EINVAL), (d
           (dict(n_q_heads=7), B.KVQ_EINVAL), (dict(n_q_heads=18), B.KVQ_EUNSUPPORTED),
           (dict(head_dim=8), B.KVQ_EUNSUPPORTED), (dict(head_dim=72), B.KVQ_EUNSUPPORTED),
           (dict(head_dim=272), B.KVQ_EUNSUPPORTED), (dict(dtype=2), B.KVQ_EINVAL), (dict(n_tokens=7), B.KVQ_EINVAL),
-          (dict(n_tokens=-1), B.KVQ_EINVAL), (dict(n_tokens=1 << 31), B.KVQ_EINVAL),
+          (dict(n_tokens=-1), B.KVQ_EINVAL), (dict(n_tokens=(1 << 30) + 1), B.KVQ_EINVAL),
           (dict(lens=(5, -1, 3)), B.KVQ_EINVAL), (dict(lens=(1 << 62, 1 << 62, 1 << 62)), B.KVQ_EINVAL),
           (dict(n_kv_heads=70000, n_q_heads=70000), B.KVQ_EUNSUPPORTED)]
 
