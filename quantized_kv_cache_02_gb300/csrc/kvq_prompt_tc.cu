@@ -33,12 +33,12 @@ constexpr float kSlack = 8.f;
 
 template <int D>
 struct TcLayout {
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kSlots = D == 128 ? 2 : 4;         // (V_j, K_j+1) pairs in flight
   static constexpr uint32_t kChunk = 128 * 128;           // 128 rows of 64 channels
   static constexpr uint32_t kTile = kChunk * (D / 64);    // a Q, K or V tile
-  static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile;
-  // barriers: full / empty per stage, then per tile: Q, S, P, PV
-  static constexpr int kNBars = 2 * kStages + 8;
+  static constexpr uint32_t kQ = 0, kK0 = 2 * kTile, kRing = 3 * kTile, kBars = kRing + 2 * kSlots * kTile;
+  // barriers: full and empty per slot, K_0, the cleared Value rows, then per tile: Q, S, P (two halves), O
+  static constexpr int kNBars = 2 * kSlots + 2 + 10;
   static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;  // + alignment
   static constexpr uint32_t kColS = 0, kColO = 256;       // S_i at 128 i, O_i at 256 + D i
 };
@@ -55,8 +55,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* smem = tc_raw + ((1024u - (smem_u32(tc_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kStages;
-  const uint32_t bar_q = bar_empty + 8 * L::kStages, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_pv = bar_p + 16;
+  const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kSlots;
+  const uint32_t bar_k0 = bar_empty + 8 * L::kSlots, bar_clear = bar_k0 + 8, bar_q = bar_clear + 8, bar_s = bar_q + 16,
+                 bar_p = bar_s + 16, bar_o = bar_p + 32;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
 
@@ -69,19 +70,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int end0 = min(sq.len, tok0 + tile_tok), end1 = min(sq.len, tok0 + 2 * tile_tok);
   const int n0 = (end0 + kKeys - 1) / kKeys, n1 = tok0 + tile_tok < sq.len ? (end1 + kKeys - 1) / kKeys : 0;
   const int nmax = max(n0, n1);
+  // Value rows of the last block past the sequence hold other sequences'
+  // values, and a weight of 0 does not silence a NaN there: the ones that the
+  // last k-step of 16 covers are cleared
+  const int valid = sq.len - (nmax - 1) * kKeys;
+  const bool clear = valid < kKeys && (valid & 15) != 0;
 
   if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
   if (t == 0) {
     *abort = 0;
-    for (int s = 0; s < L::kStages; ++s) {
+    for (int s = 0; s < L::kSlots; ++s) {
       bar_init(bar_full + 8 * s, 1);
       bar_init(bar_empty + 8 * s, 1);
     }
+    bar_init(bar_k0, 1);
+    bar_init(bar_clear, 32);
     for (int i = 0; i < 2; ++i) {
       bar_init(bar_q + 8 * i, 1);
       bar_init(bar_s + 8 * i, 1);
-      bar_init(bar_p + 8 * i, 128);
-      bar_init(bar_pv + 8 * i, 1);
+      bar_init(bar_p + 16 * i, 128);
+      bar_init(bar_p + 16 * i + 8, 128);
+      bar_init(bar_o + 8 * i, 1);
     }
     bar_init_fence();
   }
@@ -95,11 +104,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
-      // ============ copies: Q0, K0, Q1, then V_j, K_j+1 ==============================
+      // ============ copies (lane 0): Q_0, K_0, Q_1, then the pairs V_j, K_j+1 ========
+      int issued = 0;
       if (lane == 0) {
-        tma_prefetch(&maps.q);
-        tma_prefetch(&maps.k);
-        tma_prefetch(&maps.v);
         const uint32_t qbytes = (uint32_t)(tile_tok * p.g) * 128u * (D / 64);
         auto load_q = [&](int i) {
           bar_expect(bar_q + 8 * i, qbytes);
@@ -107,116 +114,111 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tma_load3(sbase + L::kQ + i * L::kTile + c * L::kChunk, &maps.q, 64 * c, h * p.g,
                       sq.start + tok0 + i * tile_tok, bar_q + 8 * i);
         };
-        int issued = 0;
-        auto load_kv = [&](const CUtensorMap* m, int blk) -> bool {
-          const int s = issued % L::kStages, round = issued / L::kStages;
-          if (round > 0 && !bar_wait(bar_empty + 8 * s, (uint32_t)(round - 1) & 1u, abort)) return false;
-          bar_expect(bar_full + 8 * s, L::kTile);
+        auto load_kv = [&](const CUtensorMap* m, uint32_t dst, int blk, uint32_t bar) {
           for (int c = 0; c < D / 64; ++c)
-            tma_load3(sbase + L::kRing + s * L::kTile + c * L::kChunk, m, 64 * c, sq.start + blk * kKeys, h,
-                      bar_full + 8 * s);
-          ++issued;
-          return true;
+            tma_load3(sbase + dst + c * L::kChunk, m, 64 * c, sq.start + blk * kKeys, h, bar);
         };
         load_q(0);
-        bool go = load_kv(&maps.k, 0);
+        bar_expect(bar_k0, L::kTile);
+        load_kv(&maps.k, L::kK0, 0, bar_k0);
         if (n1 > 0) load_q(1);
-        for (int j = 0; go && j < nmax; ++j) {
-          go = load_kv(&maps.v, j);
-          if (go && j + 1 < nmax) go = load_kv(&maps.k, j + 1);
+        for (int j = 0; j < nmax; ++j) {
+          const int s = j % L::kSlots;
+          if (j >= L::kSlots && !bar_wait(bar_empty + 8 * s, (uint32_t)(j / L::kSlots - 1) & 1u, abort)) {
+            *abort = 1;
+            if (p.status) atomicOr(p.status, kStatusPromptTimeout);
+            break;
+          }
+          const bool more = j + 1 < nmax;
+          bar_expect(bar_full + 8 * s, L::kTile * (more ? 2 : 1));
+          load_kv(&maps.v, L::kRing + 2 * s * L::kTile, j, bar_full + 8 * s);
+          if (more) load_kv(&maps.k, L::kRing + (2 * s + 1) * L::kTile, j + 1, bar_full + 8 * s);
+          ++issued;
         }
-        if (!go) *abort = 1;
-        // nothing in flight when the CTA ends (all have landed long since, unless it stops early)
-        for (int x = max(0, issued - L::kStages); x < issued; ++x)
-          bar_drain(bar_full + 8 * (x % L::kStages), (uint32_t)(x / L::kStages) & 1u);
-        bar_drain(bar_q, 0);
-        if (n1 > 0) bar_drain(bar_q + 8, 0);
       }
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      // nothing in flight when the CTA ends
+      for (int x = max(0, issued - L::kSlots); x < issued; ++x)
+        bar_drain(bar_full + 8 * (x % L::kSlots), (uint32_t)(x / L::kSlots) & 1u);
+      if (clear && issued == nmax) {
+        uint8_t* v = smem + L::kRing + 2 * ((nmax - 1) % L::kSlots) * L::kTile;
+        const int n = (16 - (valid & 15)) * 8;  // 16-byte pieces of a chunk
+        for (int x = lane; x < n * (D / 64); x += 32) {
+          const int c = x / n, y = x - c * n;
+          *reinterpret_cast<uint4*>(v + c * L::kChunk + valid * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        async_proxy_fence();
+        bar_arrive(bar_clear);
+      }
+      bar_drain(bar_k0, 0);
+      bar_drain(bar_q, 0);
+      if (n1 > 0) bar_drain(bar_q + 8, 0);
     } else if (warp == kMmaWarp) {
-      // ============ MMAs (lane 0; the other lanes help clear Value rows) =============
+      // ============ MMAs, all issued by one lane ======================================
+      // The MMAs run in the order of issue, so Q K^T of the next block may
+      // overwrite P (it shares S's columns) right behind the P V that reads it,
+      // and the arrival for S_j also says that the P V of block j - 1 is done.
       constexpr uint32_t idesc_s = bf16_idesc(kRows, kKeys, false), idesc_o = bf16_idesc(kRows, D, true);
-      int taken = 0;  // ring tiles waited for
-      auto next_tile = [&](uint32_t* addr) -> bool {
-        const int s = taken % L::kStages;
-        const bool ok = warp_wait(bar_full + 8 * s, (uint32_t)(taken / L::kStages) & 1u, abort);
-        *addr = sbase + L::kRing + s * L::kTile;
-        ++taken;
-        return ok;
-      };
+      const bool one = elect_one();
       auto scores = [&](int i, uint32_t kaddr) {
         const uint64_t a = sw128_desc(sbase + L::kQ + i * L::kTile, 0), b = sw128_desc(kaddr, 0);
-  #pragma unroll
+#pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
-          mma_ss(tm + L::kColS + 128 * i, a + off, b + off, idesc_s, ks > 0);
+          if (one) mma_ss(tm + L::kColS + 128 * i, a + off, b + off, idesc_s, ks > 0);
         }
-        mma_commit(bar_s + 8 * i);
+        if (one) mma_commit(bar_s + 8 * i);
       };
-      bool ok = true;
-      uint32_t kaddr = 0, vaddr = 0;
-      ok = next_tile(&kaddr);
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (i == 1 && n1 == 0) break;
-        ok = warp_wait(bar_q + 8 * i, 0, abort);
-        tm_fence_after();
-        if (ok && lane == 0) scores(i, kaddr);
+      auto landed = [&](int j) -> bool {
+        return bar_wait(bar_full + 8 * (j % L::kSlots), (uint32_t)(j / L::kSlots) & 1u, abort);
+      };
+      bool ok = bar_wait(bar_k0, 0, abort) && bar_wait(bar_q, 0, abort);
+      if (ok) scores(0, sbase + L::kK0);
+      if (ok && n1 > 0) {
+        ok = bar_wait(bar_q + 8, 0, abort);
+        if (ok) scores(1, sbase + L::kK0);
       }
-      if (lane == 0) mma_commit(bar_empty + 8 * ((taken - 1) % L::kStages));
-      int pv[2] = {0, 0};
+      if (ok) ok = landed(0);
       for (int j = 0; j < nmax && ok; ++j) {
-        ok = next_tile(&vaddr);
-        if (!ok) break;
-        const int vstage = (taken - 1) % L::kStages;
-        // rows of the block past the sequence hold other sequences' values: a
-        // weight of 0 does not silence a NaN there, so what a k-step of 16 covers is cleared
-        const int valid = sq.len - j * kKeys;
-        if (valid < kKeys && (valid & 15)) {
-          const int r1 = (valid + 15) & ~15;
-          for (int x = lane; x < (r1 - valid) * 8 * (D / 64); x += 32) {
-            const int c = x / ((r1 - valid) * 8), y = x - c * (r1 - valid) * 8;
-            *reinterpret_cast<uint4*>(smem + (vaddr - sbase) + c * L::kChunk + (valid + y / 8) * 128 + (y & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          async_proxy_fence();
-          __syncwarp();
-        }
-        const bool more = j + 1 < nmax;
-        if (more) ok = next_tile(&kaddr);
-        if (!ok) break;
-        for (int i = 0; i < 2; ++i) {
+        const int s = j % L::kSlots;
+        const uint32_t vaddr = sbase + L::kRing + 2 * s * L::kTile, kaddr = vaddr + L::kTile;
+        if (clear && j == nmax - 1) ok = bar_wait(bar_clear, 0, abort);
+        for (int i = 0; i < 2 && ok; ++i) {
           const int ni = i ? n1 : n0;
-          if (j < ni) {
-            if (!(ok = warp_wait(bar_p + 8 * i, (uint32_t)j & 1u, abort))) break;
-            tm_fence_after();
-            const int steps = min(8, (min(i ? end1 : end0, sq.len) - j * kKeys + 15) / 16);
-            if (lane == 0) {
-              const uint64_t b = sw128_desc(vaddr, L::kChunk);
-              for (int ks = 0; ks < steps; ++ks)
-                mma_ts(tm + L::kColO + D * i, tm + L::kColS + 128 * i + 8 * ks, b + ks * (2048 >> 4), idesc_o,
-                       j > 0 || ks > 0);
-              mma_commit(bar_pv + 8 * i);
-            }
-            ++pv[i];
-            if (j + 1 < ni) {
-              // S_i and P_i share their columns: the output MMAs have read P_i
-              if (!(ok = warp_wait(bar_pv + 8 * i, (uint32_t)j & 1u, abort))) break;
-              if (lane == 0) scores(i, kaddr);
-            }
-          }
+          if (j >= ni) continue;
+          const uint64_t b = sw128_desc(vaddr, L::kChunk);
+          const int steps = min(8, ((i ? end1 : end0) - j * kKeys + 15) / 16);
+          auto values = [&](int ks) {
+            if (one) mma_ts(tm + L::kColO + D * i, tm + L::kColS + 128 * i + 8 * ks, b + ks * (2048 >> 4), idesc_o,
+                            j > 0 || ks > 0);
+          };
+          if (!(ok = bar_wait(bar_p + 16 * i, (uint32_t)j & 1u, abort))) break;
+          tm_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            if (ks < steps) values(ks);
+          if (!(ok = bar_wait(bar_p + 16 * i + 8, (uint32_t)j & 1u, abort))) break;
+          tm_fence_after();
+#pragma unroll
+          for (int ks = 4; ks < 8; ++ks)
+            if (ks < steps) values(ks);
+          // the next pair's wait passes while MMAs are queued
+          if (i == (n1 > 0) && j + 1 < nmax) ok = landed(j + 1);
+          if (j + 1 < ni) scores(i, kaddr);
+          else if (one) mma_commit(bar_o + 8 * i);
         }
-        if (lane == 0) {
-          mma_commit(bar_empty + 8 * vstage);
-          if (more) mma_commit(bar_empty + 8 * ((taken - 1) % L::kStages));
-        }
-        __syncwarp();
+        if (ok && one) mma_commit(bar_empty + 8 * s);
       }
-      if (!ok) *abort = 1;
-      // nothing in flight when the CTA ends
-      for (int i = 0; i < 2; ++i)
-        if (pv[i] > 0) bar_drain(bar_pv + 8 * i, (uint32_t)(pv[i] - 1) & 1u);
-      if (!ok && lane == 0) {
-        mma_commit(bar_q);  // its one phase is over: a second one for this
-        bar_drain(bar_q, 1);
+      if (!ok) {
+        // stopped early: nothing in flight when the CTA ends (bar_o's first phase may be over)
+        *abort = 1;
+        if (one) {
+          if (p.status) atomicOr(p.status, kStatusPromptTimeout);
+          mma_commit(bar_o);
+          bar_drain(bar_o, 0);
+          mma_commit(bar_o);
+          bar_drain(bar_o, 1);
+        }
       }
     }
   } else {
@@ -229,6 +231,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const bool warp_live = __any_sync(0xffffffffu, live);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm + L::kColS + 128 * i + lanes, to = tm + L::kColO + D * i + lanes;
+    const float2 sc = make_float2(p.scale2, p.scale2);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -247,9 +250,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 4; c < 128; c += 4)
+        for (int c = 4; c < 124; c += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
         const bool up = top > m + kSlack;
         if (__any_sync(0xffffffffu, up)) {
@@ -257,8 +262,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (up) m = top;
           l *= a;
           if (j > 0) {
-            if (!(ok = warp_wait(bar_pv + 8 * i, (uint32_t)(j - 1) & 1u, abort))) break;
-            tm_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               float o[32];
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        const float2 sc = make_float2(p.scale2, p.scale2), nm = make_float2(-m, -m);
+        const float2 nm = make_float2(-m, -m);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -284,15 +287,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             w[e / 2] = pack_bf16(x.x, x.y);
           }
           tm_st16(ts + c / 2, w);
+          if (c == 32) {  // the first 64 keys' weights: their P V may start
+            tm_wait_st();
+            tm_fence_before();
+            bar_arrive(bar_p + 16 * i);
+          }
         }
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
         tm_wait_st();
         tm_fence_before();
+      } else {
+        bar_arrive(bar_p + 16 * i);
       }
-      bar_arrive(bar_p + 8 * i);
+      bar_arrive(bar_p + 16 * i + 8);
     }
-    if (ok && n > 0) ok = warp_wait(bar_pv + 8 * i, (uint32_t)(n - 1) & 1u, abort);
+    if (ok && n > 0) ok = warp_wait(bar_o + 8 * i, 0, abort);
     if (!ok) {
       *abort = 1;
       if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);

@@ -177,46 +177,50 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (pr == 0 || !resident)
           for (int i = q_first(pr); i < nq && go; i += p.split) load_q(i, i + p.split < nq ? i + p.split : -1);
       }
-      if (!go) *abort = 1;
+      if (!go) {
+        *abort = 1;
+        if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
+      }
       // nothing in flight when the CTA ends
       for (int x = max(0, kpairs - 2); x < kpairs; ++x) bar_drain(bar_kf + 8 * (x & 1), (uint32_t)(x / 2) & 1u);
       for (int x = max(0, issued - kQStages); x < issued; ++x)
         bar_drain(bar_qf + 8 * (x % kQStages), (uint32_t)(x / kQStages) & 1u);
     } else if (warp == kMmaWarp) {
-      // ============ MMAs (lane 0) =======================================================
+      // ============ MMAs, all issued by one lane ========================================
+      const bool one = elect_one();
       constexpr uint32_t idesc = bf16_idesc(kKeys, kRows, false);
       int taken = 0, n_s[2] = {0, 0};
       bool ok = true;
       for (int pr = 0; pr < pairs && ok; ++pr) {
         const int both = run0 + pr * 2 * kKeys + kKeys < sq.len;
-        ok = warp_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort);
+        ok = bar_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort);
         for (int i = q_first(pr); i < nq && ok; i += p.split) {
           const int s = resident ? i : taken % kQStages;
-          ok = warp_wait(bar_qf + 8 * s, resident ? 0u : (uint32_t)(taken / kQStages) & 1u, abort);
+          ok = bar_wait(bar_qf + 8 * s, resident ? 0u : (uint32_t)(taken / kQStages) & 1u, abort);
           ++taken;
           for (int w = 0; w < 1 + both && ok; ++w) {
             const int b = 2 * w + (n_s[w] & 1);
-            if (n_s[w] > 1) ok = warp_wait(bar_se + 8 * b, (uint32_t)(n_s[w] / 2 - 1) & 1u, abort);
+            if (n_s[w] > 1) ok = bar_wait(bar_se + 8 * b, (uint32_t)(n_s[w] / 2 - 1) & 1u, abort);
             if (!ok) break;
             tm_fence_after();
-            if (lane == 0) {
-              const uint64_t da = sw128_desc(sbase + k_tile(pr, w), 0);
-              const uint64_t db = sw128_desc(sbase + q_tile(s), 0);
+            const uint64_t da = sw128_desc(sbase + k_tile(pr, w), 0);
+            const uint64_t db = sw128_desc(sbase + q_tile(s), 0);
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
-                mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > 0);
-              }
-              mma_commit(bar_sf + 8 * b);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
+              if (one) mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > 0);
             }
+            if (one) mma_commit(bar_sf + 8 * b);
             ++n_s[w];
           }
-          if (lane == 0 && !resident) mma_commit(bar_qe + 8 * s);
+          if (one && !resident) mma_commit(bar_qe + 8 * s);
         }
-        if (lane == 0) mma_commit(bar_ke + 8 * (pr & 1));
-        __syncwarp();
+        if (one) mma_commit(bar_ke + 8 * (pr & 1));
       }
-      if (!ok) *abort = 1;
+      if (!ok) {
+        *abort = 1;
+        if (one && p.status) atomicOr(p.status, kStatusPromptTimeout);
+      }
       // nothing in flight when the CTA ends: the last commit on a score buffer covers the MMAs before it
       for (int w = 0; w < 2; ++w)
         for (int x = max(0, n_s[w] - 2); x < n_s[w]; ++x) bar_drain(bar_sf + 8 * (2 * w + (x & 1)), (uint32_t)(x / 2) & 1u);
