@@ -58,7 +58,7 @@ struct PromptParams {
   float* weights;              // [Hkv][n_tokens]
   int64_t n_tokens;
   int64_t last;                // weights: queries counted back from each sequence's end
-  float lse_hi, lse_lo;        // weights: sqrt(D) * scale2 as two floats, lse times it is in the scores' units
+  float lse_hi, lse_lo;        // weights: lse times their sum is in the scores' units
   int32_t split;               // weights on the tensor cores: CTAs that share a pair of key tiles
   int32_t* status;
   PromptTiles tiles;

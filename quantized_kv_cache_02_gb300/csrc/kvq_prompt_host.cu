@@ -186,8 +186,10 @@ void base_params(const kvq_prompt* p, kvq::PromptParams* pp) {
   pp->g = p->n_q_heads / p->n_kv_heads;
   const double loss = tensor_cores(p) ? rounding_loss(p->head_dim) : 0.0;
   pp->scale2 = (float)(1.4426950408889634 / std::sqrt((double)p->head_dim) * (1.0 + loss));
-  // lse in the scores' units is sqrt(d) scale2 / (1 + loss) lse, the factor as two floats
-  const double r = std::sqrt((double)p->head_dim) * (double)pp->scale2 / (1.0 + loss);
+  // lse in the units of the scores -- on the tensor cores before scale2, else after it -- is this
+  // factor times lse, as two floats
+  const double r = tensor_cores(p) ? std::sqrt((double)p->head_dim) / (1.0 + loss)
+                                   : std::sqrt((double)p->head_dim) * (double)pp->scale2;
   pp->lse_hi = (float)r;
   pp->lse_lo = (float)(r - (double)pp->lse_hi);
   pp->q_ts = p->q_token_stride;

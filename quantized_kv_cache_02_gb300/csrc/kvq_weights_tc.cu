@@ -18,14 +18,16 @@
 // their sums in rank order, so a short prompt fills the GPU and the result
 // has the same bits every time.
 //
-// Exponent: with the rounded factor c ~ log2(e) / sqrt(d), s c - L and
-// L = lse sqrt(d) c differ from the exact exponent only by a factor 1 + 2^-24
-// on what is near 0 where a weight counts.  L is kept as a float and the
-// remainder enters as the factor 2^-rest on the row's terms (one fused
-// multiply-add in place of the sum's addition).
+// The row's L_r enters in the MMA: one more k-step of 16 takes it off every
+// score, as four bf16 pieces against a column of ones, so an element costs one
+// multiplication, one exponential and one addition, and no load of its own.
+// (Read per column from shared memory instead, the loads took the bandwidth that
+// the MMAs' operands need: 123 us against NEWTIME for 4096 whole tokens, 32/8
+// heads of 128.)
 // ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d) + M).)
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_prompt.h"
 #include "kvq_tcgen05.cuh"
@@ -44,8 +46,10 @@ struct WLayout {
   static constexpr uint32_t kTile = kChunk * (D / 64);
   // what streams, and what stays: two key pairs past two query tiles, or four query tiles past one key pair
   static constexpr uint32_t kStream = 0, kStay = 4 * kTile;
-  static constexpr uint32_t kL = kStay + 2 * kTile;              // per query tile 64 x {L0, L1, f0, f1}
-  static constexpr uint32_t kRed = kL + kQStages * 1024;           // [8 ranks][256 keys]
+  // the last k-step's operands, 8 rows x 16 bytes a core matrix: columns 0-7 of
+  // -L per query tile and of ones, and the zeros of columns 8-15 of both
+  static constexpr uint32_t kL = kStay + 2 * kTile, kOnes = kL + kQStages * 2048, kZero = kOnes + 2048;
+  static constexpr uint32_t kRed = kZero + 2048;                 // [8 ranks][256 keys]
   static constexpr uint32_t kBars = kRed + 8 * 256 * 4;
   // K full / empty (2 each), Q full / empty, S full / empty (tile, buffer)
   static constexpr int kNBars = 4 + 2 * kQStages + 8;
@@ -95,14 +99,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
       bar_init(bar_ke + 8 * i, 1);
     }
     for (int i = 0; i < kQStages; ++i) {
-      bar_init(bar_qf + 8 * i, 1 + 32);  // the copy, and the lanes that wrote L
-      bar_init(bar_qe + 8 * i, 1 + 8);   // the MMAs, and the summing warps
+      bar_init(bar_qf + 8 * i, 1 + 32);  // the copy, and the lanes that wrote -L
+      bar_init(bar_qe + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) {
       bar_init(bar_sf + 8 * i, 1);
       bar_init(bar_se + 8 * i, 128);
     }
     bar_init_fence();
+  }
+  if (t < 256) {
+    *reinterpret_cast<uint4*>(smem + L::kOnes + t * 16) =
+        t < 128 ? make_uint4(0x3f803f80u, 0x3f803f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    async_proxy_fence();
   }
   tm_fence_before();
   __syncthreads();
@@ -116,7 +125,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
-      // ============ copies; the lanes turn lse into L =================================
+      // ============ copies; the lanes turn lse into -L =================================
       if (lane == 0) {
         tma_prefetch(&maps.q);
         tma_prefetch(&maps.k);
@@ -151,14 +160,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
             tma_load3(sbase + q_tile(s) + c * L::kChunk, &maps.q, 64 * c, h * p.g,
                       sq.start + tok0 + i * tile_tok, bar_qf + 8 * s);
         }
-        float* dst = reinterpret_cast<float*>(smem + L::kL + s * 1024);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 32 * e + lane;
-          const float hi = __fmul_rn(now[e], p.lse_hi), rest = fmaf(now[e], p.lse_hi, -hi) + now[e] * p.lse_lo;
-          dst[(r >> 1) * 4 + (r & 1)] = hi;
-          dst[(r >> 1) * 4 + 2 + (r & 1)] = ex2(-rest);
+          // -L = -lse * lse_hi - lse * lse_lo, cut into four pieces of 8 bits
+          const float hi = __fmul_rn(-now[e], p.lse_hi), rest = fmaf(-now[e], p.lse_hi, -hi) - now[e] * p.lse_lo;
+          const float b0 = __bfloat162float(__float2bfloat16_rn(hi)), left = hi - b0;
+          const float b1 = __bfloat162float(__float2bfloat16_rn(left)), last = left - b1 + rest;
+          const float b2 = __bfloat162float(__float2bfloat16_rn(last));
+          *reinterpret_cast<uint4*>(smem + L::kL + s * 2048 + (32 * e + lane) * 16) =
+              make_uint4(pack_bf16(b0, b1), pack_bf16(b2, last - b2), 0u, 0u);
         }
+        async_proxy_fence();
         bar_arrive(bar_qf + 8 * s);
         ++issued;
       };
@@ -210,7 +222,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
               const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
               if (one) mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > 0);
             }
-            if (one) mma_commit(bar_sf + 8 * b);
+            if (one) {
+              mma_ss(tm + 128 * b, plain_desc(sbase + L::kOnes, 2048),
+                     plain_desc(sbase + L::kL + s * 2048, L::kZero - L::kL - s * 2048), idesc, 1);
+              mma_commit(bar_sf + 8 * b);
+            }
             ++n_s[w];
           }
           if (one && !resident) mma_commit(bar_qe + 8 * s);
@@ -231,28 +247,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int w = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float2 sc = make_float2(p.scale2, p.scale2);
-    int taken = 0, n_s = 0;
+    int n_s = 0;
     bool ok = true;
     for (int pr = 0; pr < pairs && ok; ++pr) {
       const int tile_key = run0 + pr * 2 * kKeys + w * kKeys, key = tile_key + (t & 127);
       const bool active = tile_key < sq.len;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      for (int i = q_first(pr); i < nq && ok; i += p.split) {
-        const int s = resident ? i : taken % kQStages;
-        const uint32_t qpar = resident ? 0u : (uint32_t)(taken / kQStages) & 1u;
-        ++taken;
-        if (active) {
-          const int b = 2 * w + (n_s & 1);
-          ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n_s / 2) & 1u, abort) && warp_wait(bar_qf + 8 * s, qpar, abort);
-          if (!ok) break;
-          ++n_s;
-          tm_fence_after();
-          // rows [lo, hi) of the tile count for this key
-          const int pos0 = tok0 + i * tile_tok;
-          const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
-          const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
-          const float4* lf = reinterpret_cast<const float4*>(smem + L::kL + s * 1024);
-          const uint32_t ts = tm + 128 * b + lanes;
+      for (int i = q_first(pr); i < nq && active; i += p.split) {
+        const int b = 2 * w + (n_s & 1);
+        if (!(ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n_s / 2) & 1u, abort))) break;
+        ++n_s;
+        tm_fence_after();
+        // rows [lo, hi) of the tile count for this key
+        const int pos0 = tok0 + i * tile_tok;
+        const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
+        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
+        const uint32_t ts = tm + 128 * b + lanes;
+        auto add_tile = [&](auto with_mask) {
           float x[2][32];
           tm_ld32(ts, x[0]);
 #pragma unroll
@@ -261,25 +272,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
             if (c < 3) tm_ld32(ts + 32 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float4 f = lf[16 * c + e / 2];
-              float2 y = fma2(make_float2(x[c & 1][e], x[c & 1][e + 1]), sc, make_float2(-f.x, -f.y));
+              float2 y = mul2(make_float2(x[c & 1][e], x[c & 1][e + 1]), sc);
               y.x = ex2(y.x);
               y.y = ex2(y.y);
-              if (masked) {
+              if (decltype(with_mask)::value) {
                 const int r = 32 * c + e;
                 y.x = r >= lo && r < hi ? y.x : 0.f;
                 y.y = r + 1 >= lo && r + 1 < hi ? y.y : 0.f;
               }
-              sum[(e >> 1) & 1] = fma2(y, make_float2(f.z, f.w), sum[(e >> 1) & 1]);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
             }
           }
-          tm_fence_before();
-          bar_arrive(bar_se + 8 * b);
-        }
-        if (!resident) {
-          __syncwarp();
-          if (lane == 0) bar_arrive(bar_qe + 8 * s);
-        }
+        };
+        if (masked) add_tile(std::true_type());
+        else add_tile(std::false_type());
+        tm_fence_before();
+        bar_arrive(bar_se + 8 * b);
       }
       if (!ok) break;
       sum[0] = add2(sum[0], sum[1]);
