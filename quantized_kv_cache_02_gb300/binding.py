@@ -8,6 +8,7 @@ library has not been built; there is no other implementation to fall back on.
 from __future__ import annotations
 
 import ctypes
+import numbers
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -299,16 +300,19 @@ def kvq_evict(prompt: kvq_prompt, k_ptr, v_ptr, weights_ptr, keep, first, recent
 
 
 # ---- prompt operators on torch tensors ---------------------------------------
+#
+# A short prompt's call is bound by the host (the kernels take 5 to 15 us), so
+# these read each attribute of a tensor once.
 
 _prompt_status = {}  # device index -> int32 status word that the prompt kernels report to
 
 
-def _status_word(device):
+def _status_word(device_index):
     import torch
-    word = _prompt_status.get(device.index)
+    word = _prompt_status.get(device_index)
     if word is None and not torch.cuda.is_current_stream_capturing():
-        word = _prompt_status[device.index] = torch.zeros(1, dtype=torch.int32, device=device)
-        torch.cuda.synchronize(device)  # cleared before any stream can report to it
+        word = _prompt_status[device_index] = torch.zeros(1, dtype=torch.int32, device=f"cuda:{device_index}")
+        torch.cuda.synchronize(device_index)  # cleared before any stream can report to it
     return word  # None in a capture that no eager call came before: those kernels report nowhere
 
 
@@ -316,48 +320,74 @@ def prompt_status(device=None) -> int:
     """The prompt kernels' status word on a device (synchronizes): 0 unless a
     bounded wait gave up there since the process started."""
     import torch
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(device):
-        return int(_status_word(torch.device("cuda", torch.cuda.current_device())).item())
+        return int(_status_word(torch.cuda.current_device()).item())
 
 
-def _check_packed(name, t, like=None):
-    assert t.is_cuda and t.dim() == 3, f"{name} must be a CUDA tensor [tokens, heads, head_dim]"
-    assert t.stride(2) == 1 or t.shape[2] == 1, f"{name}'s last dimension must be contiguous"
-    if like is not None:
-        assert t.device == like.device and t.dtype == like.dtype, f"{name} must match the device and dtype of k"
-        assert t.shape[0] == like.shape[0] and t.shape[2] == like.shape[2], \
-            f"{name} must have k's tokens and head_dim, got {tuple(t.shape)}"
+def _counts(values):
+    try:
+        return (ctypes.c_int64 * len(values))(*values)
+    except TypeError:  # integers of other kinds (numpy, tensors)
+        return _i64_array(values)
 
 
-def _prompt(k, seq_lens, q=None, v=None, out=None):
-    import torch
-    _check_packed("k", k)
-    dtypes = {torch.bfloat16: KVQ_BF16, torch.float32: KVQ_FP32}
-    assert k.dtype in dtypes, f"expected bfloat16 or float32, got {k.dtype}"
-    lens = _i64_array(seq_lens)
-    p = kvq_prompt(len(lens), k.shape[1], k.shape[1], k.shape[2], dtypes[k.dtype], lens, k.shape[0])
-    p.k_token_stride, p.k_head_stride = k.stride(0), k.stride(1)
-    if q is not None:
-        _check_packed("q", q, k)
-        p.n_q_heads, p.q_token_stride, p.q_head_stride = q.shape[1], q.stride(0), q.stride(1)
-    if v is not None:
-        _check_packed("v", v, k)
-        assert v.shape == k.shape, f"v must have k's shape, got {tuple(v.shape)}"
-        p.v_token_stride, p.v_head_stride = v.stride(0), v.stride(1)
-    if out is not None:
-        _check_packed("out", out, k)
-        assert out.shape == q.shape, f"out must have q's shape, got {tuple(out.shape)}"
-        p.out_token_stride, p.out_head_stride = out.stride(0), out.stride(1)
-    word = _status_word(k.device)
-    p.status = None if word is None else word.data_ptr()
-    return p
+class _Prompt:
+    """The checked arguments of one prompt operator: the C struct, and how to
+    call on k's device and torch's current stream there."""
 
+    __slots__ = ("torch", "c", "k", "device", "tokens", "heads", "dim")
 
-def _check_rows(name, t, rows, k):
-    assert t.device == k.device and t.is_contiguous() and str(t.dtype) == "torch.float32", \
-        f"{name} must be a contiguous float32 tensor on k's device"
-    assert tuple(t.shape) == (rows, k.shape[0]), f"expected {name} of shape {(rows, k.shape[0])}, got {tuple(t.shape)}"
+    def __init__(self, k, seq_lens):
+        import torch
+        self.torch, self.k = torch, k
+        assert k.is_cuda and k.dim() == 3, "k must be a CUDA tensor [tokens, heads, head_dim]"
+        dtype = k.dtype
+        assert dtype == torch.bfloat16 or dtype == torch.float32, f"expected bfloat16 or float32, got {dtype}"
+        self.device = k.get_device()
+        self.tokens, self.heads, self.dim = k.shape
+        lens = _counts(seq_lens)
+        self.c = c = kvq_prompt(len(lens), self.heads, self.heads, self.dim,
+                                KVQ_BF16 if dtype == torch.bfloat16 else KVQ_FP32, lens, self.tokens)
+        c.k_token_stride, c.k_head_stride = self.strides("k", k, None)
+        word = _prompt_status.get(self.device)
+        if word is None:
+            word = _status_word(self.device)
+        if word is not None:
+            c.status = word.data_ptr()
+
+    def strides(self, name, t, heads):
+        shape, stride, k = t.shape, t.stride(), self.k
+        assert len(shape) == 3 and shape[0] == self.tokens and shape[2] == self.dim and heads in (None, shape[1]), \
+            f"{name} of shape {tuple(shape)} does not go with k of shape {tuple(k.shape)}"
+        assert t.get_device() == self.device and t.dtype == k.dtype, f"{name} must match the device and dtype of k"
+        assert stride[2] == 1, f"{name}'s last dimension must be contiguous"
+        return stride[:2]
+
+    def queries(self, q):
+        self.c.n_q_heads = q.shape[1]
+        self.c.q_token_stride, self.c.q_head_stride = self.strides("q", q, None)
+
+    def values(self, v):
+        self.c.v_token_stride, self.c.v_head_stride = self.strides("v", v, self.heads)
+
+    def rows(self, name, t, heads):
+        """A float32 [heads, tokens] tensor; made where t is None."""
+        torch = self.torch
+        if t is None:
+            return torch.empty((heads, self.tokens), dtype=torch.float32, device=self.k.device)
+        assert t.dtype == torch.float32 and t.is_contiguous() and t.get_device() == self.device, \
+            f"{name} must be a contiguous float32 tensor on k's device"
+        assert t.shape == (heads, self.tokens), f"expected {name} of shape {(heads, self.tokens)}, got {tuple(t.shape)}"
+        return t
+
+    def call(self, fn, *args):
+        cuda = self.torch.cuda
+        if cuda.current_device() != self.device:
+            with cuda.device(self.device):
+                return self.call(fn, *args)
+        status = fn(ctypes.byref(self.c), *args, self.torch._C._cuda_getCurrentRawStream(self.device))
+        if status:
+            _check(status)
 
 
 def prompt_attention(q, k, v, seq_lens, out=None, lse=None):
@@ -365,17 +395,15 @@ def prompt_attention(q, k, v, seq_lens, out=None, lse=None):
     k, v [tokens, n_kv_heads, head_dim] (bf16 or fp32; any strides of whole
     16-byte steps), seq_lens the sequences' lengths in order.  Returns (out,
     lse): out like q, lse float32 [n_q_heads, tokens]."""
-    import torch
+    p = _Prompt(k, seq_lens)
+    p.queries(q)
+    p.values(v)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    p = _prompt(k, seq_lens, q, v, out)
-    if lse is None:
-        lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
-    else:
-        _check_rows("lse", lse, q.shape[1], k)
-    with torch.cuda.device(k.device):
-        kvq_prompt_attention(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                             torch.cuda.current_stream(k.device).cuda_stream)
+        out = p.torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    p.c.out_token_stride, p.c.out_head_stride = p.strides("out", out, q.shape[1])
+    lse = p.rows("lse", lse, q.shape[1])
+    p.call(load_library().kvq_prompt_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+           lse.data_ptr())
     return out, lse
 
 
@@ -383,16 +411,12 @@ def prompt_weights(q, k, lse, seq_lens, last, out=None):
     """The attention weight every prompt token gathers from the last ``last``
     queries of its sequence, summed over the query heads of its KV head
     (float32 [n_kv_heads, tokens]); lse as prompt_attention returned it."""
-    import torch
-    p = _prompt(k, seq_lens, q)
-    _check_rows("lse", lse, q.shape[1], k)
-    if out is None:
-        out = torch.empty(k.shape[1], k.shape[0], dtype=torch.float32, device=k.device)
-    else:
-        _check_rows("out", out, k.shape[1], k)
-    with torch.cuda.device(k.device):
-        kvq_prompt_weights(p, q.data_ptr(), k.data_ptr(), lse.data_ptr(), last, out.data_ptr(),
-                           torch.cuda.current_stream(k.device).cuda_stream)
+    assert lse is not None, "lse is needed"
+    p = _Prompt(k, seq_lens)
+    p.queries(q)
+    p.rows("lse", lse, q.shape[1])
+    out = p.rows("out", out, p.heads)
+    p.call(load_library().kvq_prompt_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(), last, out.data_ptr())
     return out
 
 
@@ -419,20 +443,21 @@ def evict(k, v, weights, seq_lens, keep, first=0, recent=0):
     ``recent`` and the heaviest between, equal weights by lowest token.  k, v
     [tokens, n_kv_heads, head_dim]; weights float32 [n_kv_heads, tokens].
     Returns a Kept."""
-    import torch
-    p = _prompt(k, seq_lens, v=v)
-    _check_rows("weights", weights, k.shape[1], k)
-    lens = list(seq_lens)
-    counts = [min(int(keep), int(n)) for n in lens] if isinstance(keep, int) else [int(n) for n in keep]
-    assert len(counts) == len(lens), f"expected {len(lens)} counts in keep, got {len(counts)}"
-    rows = max(0, sum(counts)) * k.shape[1]
-    k_out = torch.empty(rows, k.shape[2], dtype=k.dtype, device=k.device)
+    assert weights is not None, "weights are needed"
+    p = _Prompt(k, seq_lens)
+    p.values(v)
+    p.rows("weights", weights, p.heads)
+    counts = [min(int(keep), int(n)) for n in seq_lens] if isinstance(keep, numbers.Integral) else [int(n) for n in keep]
+    assert len(counts) == len(seq_lens), f"expected {len(seq_lens)} counts in keep, got {len(counts)}"
+    torch, device = p.torch, k.device
+    rows = max(0, sum(counts)) * p.heads
+    k_out = torch.empty((rows, p.dim), dtype=k.dtype, device=device)
     v_out = torch.empty_like(k_out)
-    index = torch.empty(rows, dtype=torch.int32, device=k.device)
-    with torch.cuda.device(k.device):
-        kvq_evict(p, k.data_ptr(), v.data_ptr(), weights.data_ptr(), counts, first, recent, k_out.data_ptr(),
-                  v_out.data_ptr(), index.data_ptr(), torch.cuda.current_stream(k.device).cuda_stream)
-    return Kept(k_out, v_out, index, counts, k.shape[1])
+    index = torch.empty(rows, dtype=torch.int32, device=device)
+    p.call(load_library().kvq_evict, k.data_ptr(), v.data_ptr(), weights.data_ptr(),
+           _counts(counts), first, recent, k_out.data_ptr(), v_out.data_ptr(),
+           index.data_ptr())
+    return Kept(k_out, v_out, index, counts, p.heads)
 
 
 def kvq_kernel_launches() -> int:
