@@ -5,10 +5,13 @@
 // Choice.  The first ``first`` and the last ``recent`` tokens stay; of the ones
 // between, the ``left`` heaviest, equal weights by lowest token.  A cluster of up
 // to 16 CTAs takes a unit, a run of its tokens each, kept in shared memory as
-// order-preserving words.  A radix select finds the left-th largest word in
-// passes of 11, 11 and 10 bits (each CTA counts its run, all read every CTA's
-// counts through distributed shared memory: one cluster barrier a pass); one
-// ordered pass then writes the kept tokens.  Every weight is read once.
+// order-preserving words.  A radix select finds the left-th largest word eight
+// bits at a time (each CTA counts its run, all add up every CTA's 256 counts
+// through distributed shared memory: one cluster barrier a pass); one ordered
+// pass then writes the kept tokens.  Every weight is read once.  With 256
+// counters two CTAs of 27,000 words fit an SM and eight units of 432,000 tokens
+// run at once: SELTIME; passes of 11 bits, whose 2048 counters read
+// from 16 peers took 10 us a pass and whose clusters came in two waves, 163 us.
 //
 // Gather.  A thread has four 16-byte pieces of K and of V in flight.  Bound by
 // HBM: 16 bytes a kept piece read and written.  Small choices gather in the
@@ -22,9 +25,8 @@ namespace kvq {
 namespace {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
 constexpr int kMaxCluster = 16;
-constexpr int kCached = 48 * 1024;   // words of a run that shared memory holds; a longer one is read again a pass
+constexpr int kCached = 55 * 1024;   // words of a run that shared memory holds; a longer one is read again a pass
 constexpr int kGatherThreads = 256, kPieces = 4 * kGatherThreads;
 
 // Weights in increasing order as unsigned words: -0 equals 0, NaN is lowest.
@@ -35,16 +37,18 @@ __device__ __forceinline__ uint32_t order_bits(float w) {
 }
 
 struct SelShared {
-  uint32_t hist[3][kBins];
-  uint32_t warp_sum[kSelWarps];
-  uint32_t above[kSelWarps], equal[kSelWarps];  // kept and tied words of each warp's stretch
+  uint32_t hist[4][256];                        // the CTA's counts, a pass each
+  uint32_t sums[256];                           // the cluster's
+  uint32_t above[kSelWarps], equal[kSelWarps];  // running sums of each warp's kept and tied words
   uint32_t totals[2];                           // of the CTA
   uint32_t digit, rank;
 };
+static_assert(sizeof(SelShared) + kCached * sizeof(uint32_t) <= 227 * 1024, "a run has to fit shared memory");
 
-__device__ __forceinline__ void cluster_barrier(int size) {
+template <bool CLUSTER>
+__device__ __forceinline__ void unit_barrier() {
   __syncwarp();
-  if (size > 1)
+  if (CLUSTER)
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   else
     __syncthreads();
@@ -59,25 +63,18 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, int rank) {
   return v;
 }
 
-// Sum over the threads before this one (and, in *all, over all).
-__device__ __forceinline__ uint32_t scan_before(uint32_t x, SelShared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t incl = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
-  }
-  if (lane == 31) sh.warp_sum[warp] = incl;
-  __syncthreads();
-  uint32_t w = sh.warp_sum[lane];
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, w, d);
-    if (lane >= d) w += y;
-  }
-  const uint32_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-  return incl - x + (warp > 0 ? before : 0u);
+// Four words of another rank's shared memory.
+__device__ __forceinline__ uint4 peer_words(const uint32_t* p, int rank) {
+  uint32_t a;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
 }
 
 // Copy kept rows [r0, r0 + rows) of a unit.
@@ -109,15 +106,18 @@ __device__ __forceinline__ void gather_rows(const EvictParams& p, const EvictSeq
   }
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+// CLUSTER: a cluster a unit, two CTAs an SM; else one CTA, which may also copy the rows.
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kSelThreads, CLUSTER ? 2 : 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint8_t sel_smem[];
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_smem);
   uint32_t* run = reinterpret_cast<uint32_t*>(sel_smem + sizeof(SelShared));
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int size = gridDim.x, rank = blockIdx.x, h = blockIdx.y;  // a cluster is one unit
+  const int size = CLUSTER ? gridDim.x : 1, rank = CLUSTER ? blockIdx.x : 0, h = blockIdx.y;  // a cluster is one unit
   const EvictSeq sq = p.seq[blockIdx.z];
   int32_t* out = p.index + sq.out_row + (int64_t)h * sq.keep;
-  for (int i = t; i < 3 * kBins; i += kSelThreads) sh.hist[0][i] = 0;
+  sh.hist[0][t] = 0;  // 1024 counters
+  if (t < 256) sh.sums[t] = 0;
   pdl_wait();
   pdl_release();
   if (sq.keep >= sq.len) {  // nothing is evicted
@@ -134,77 +134,102 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       const bool cached = share <= kCached;
       auto word = [&](int i) { return cached ? run[i] : order_bits(w[i]); };
       __syncthreads();
+      for (int i0 = t; i0 < n; i0 += 8 * kSelThreads) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = i0 + e * kSelThreads < n ? __ldcs(w + i0 + e * kSelThreads) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = i0 + e * kSelThreads;
+          if (i < n) {
+            const uint32_t o = order_bits(x[e]);
+            if (cached) run[i] = o;
+            atomicAdd(&sh.hist[0][o >> 24], 1u);
+          }
+        }
+      }
       uint32_t prefix = 0, need = left;
 #pragma unroll 1
-      for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t mask = pass == 2 ? 1023u : 2047u;
+      for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
         uint32_t* hist = sh.hist[pass];
-        const int whole = (n + kSelThreads - 1) / kSelThreads * kSelThreads;
+        if (pass > 0) {
 #pragma unroll 4
-        for (int i = t; i < whole; i += kSelThreads) {
-          bool in = i < n;
-          uint32_t x = 0;
-          if (in) {
-            if (pass == 0) {
-              x = order_bits(__ldcs(w + i));
-              if (cached) run[i] = x;
-            } else {
-              x = word(i);
-              in = x >> (pass == 1 ? 21 : 10) == prefix;
+          for (int i = t; i < n; i += kSelThreads) {
+            const uint32_t x = word(i);
+            if (x >> (shift + 8) == prefix) atomicAdd(&hist[(x >> shift) & 255u], 1u);
+          }
+        }
+        unit_barrier<CLUSTER>();
+        const uint32_t* sums = hist;
+        if (CLUSTER) {
+          // 64 threads a rank, four counters each
+          if (t < 64 * size) {
+            const uint4 c = peer_words(hist + 4 * (t & 63), t >> 6);
+            if (c.x) atomicAdd(&sh.sums[4 * (t & 63)], c.x);
+            if (c.y) atomicAdd(&sh.sums[4 * (t & 63) + 1], c.y);
+            if (c.z) atomicAdd(&sh.sums[4 * (t & 63) + 2], c.z);
+            if (c.w) atomicAdd(&sh.sums[4 * (t & 63) + 3], c.w);
+          }
+          __syncthreads();
+          sums = sh.sums;
+        }
+        if (warp == 0) {
+          // lane l holds digits 255 - 8 l .. 248 - 8 l; find where the count from the top passes the rank
+          uint32_t c[8], mine = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mine += c[e] = sums[255 - 8 * lane - e];
+          uint32_t incl = mine;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+          }
+          uint32_t before = incl - mine;
+          if (before < need && need <= incl) {
+            int digit = 255 - 8 * lane;
+#pragma unroll
+            for (int e = 0; e < 7; ++e) {
+              if (digit == 255 - 8 * lane - e && before + c[e] < need) {
+                before += c[e];
+                --digit;
+              }
             }
+            sh.digit = (uint32_t)digit;
+            sh.rank = need - before;
           }
-          const uint32_t d = (x >> shift) & mask;
-          // equal weights (a prompt's many zeros) would queue up at one counter
-          int same;
-          __match_all_sync(0xffffffffu, in ? d : ~0u, &same);
-          if (same) {
-            if (lane == 0 && in) atomicAdd(&hist[d], 32u);
-          } else if (in) {
-            atomicAdd(&hist[d], 1u);
-          }
-        }
-        cluster_barrier(size);
-        // bins from the top, two a thread, over the cluster
-        uint32_t c0 = 0, c1 = 0;
-        const int b0 = kBins - 1 - 2 * t;
-        if (size > 1) {
-#pragma unroll 4
-          for (int r = 0; r < size; ++r) {
-            c0 += peer_word(hist + b0, r);
-            c1 += peer_word(hist + b0 - 1, r);
-          }
-        } else {
-          c0 = hist[b0];
-          c1 = hist[b0 - 1];
-        }
-        const uint32_t before = scan_before(c0 + c1, sh);
-        if (before < need && need <= before + c0 + c1) {
-          const bool second = need > before + c0;
-          sh.digit = (uint32_t)(second ? b0 - 1 : b0);
-          sh.rank = need - before - (second ? c0 : 0u);
         }
         __syncthreads();
-        prefix = pass == 2 ? prefix << 10 | sh.digit : prefix << 11 | sh.digit;
+        prefix = prefix << 8 | sh.digit;
         need = sh.rank;
-        __syncthreads();
+        if (t < 256) sh.sums[t] = 0;  // warp 0 is done with them, and the next pass adds behind a barrier
       }
-      // Words above the left-th largest stay, and the first ``need`` equal to it.
-      // Each warp counts a stretch of the run, then writes it in order.
-      const int stretch = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31, s0 = min(n, warp * stretch),
-                s1 = min(n, s0 + stretch);
+      // Words above the left-th largest stay, and the first ``need`` equal to
+      // it.  A thread counts a stretch of the run (of odd length: no two lanes on
+      // one bank), then writes its kept tokens from where those before it end.
+      const int stretch = (n + kSelThreads - 1) / kSelThreads | 1, s0 = min(n, t * stretch), s1 = min(n, s0 + stretch);
       uint32_t above = 0, equal = 0;
-      for (int i0 = s0; i0 < s1; i0 += 32) {
-        const uint32_t x = i0 + lane < s1 ? word(i0 + lane) : 0u;
-        above += __popc(__ballot_sync(0xffffffffu, i0 + lane < s1 && x > prefix));
-        equal += __popc(__ballot_sync(0xffffffffu, i0 + lane < s1 && x == prefix));
+#pragma unroll 4
+      for (int i = s0; i < s1; ++i) {
+        const uint32_t x = word(i);
+        above += x > prefix;
+        equal += x == prefix;
       }
-      if (lane == 0) {
-        sh.above[warp] = above;
-        sh.equal[warp] = equal;
+      uint32_t n_above = above, n_equal = equal;  // running sums over the threads, this one's included
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t ya = __shfl_up_sync(0xffffffffu, n_above, d), ye = __shfl_up_sync(0xffffffffu, n_equal, d);
+        if (lane >= d) {
+          n_above += ya;
+          n_equal += ye;
+        }
+      }
+      if (lane == 31) {
+        sh.above[warp] = n_above;
+        sh.equal[warp] = n_equal;
       }
       __syncthreads();
-      uint32_t wa = sh.above[lane], we = sh.equal[lane];  // running sums over the warps
+      uint32_t wa = sh.above[lane], we = sh.equal[lane];
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const uint32_t ya = __shfl_up_sync(0xffffffffu, wa, d), ye = __shfl_up_sync(0xffffffffu, we, d);
@@ -217,30 +242,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         sh.totals[0] = wa;
         sh.totals[1] = we;
       }
-      uint32_t n_above = __shfl_sync(0xffffffffu, wa, warp) - above, n_equal = __shfl_sync(0xffffffffu, we, warp) - equal;
-      cluster_barrier(size);
-      if (size > 1) {
-        for (int r = 0; r < rank; ++r) {
-          n_above += peer_word(&sh.totals[0], r);
-          n_equal += peer_word(&sh.totals[1], r);
+      wa = __shfl_sync(0xffffffffu, wa, max(warp - 1, 0));
+      we = __shfl_sync(0xffffffffu, we, max(warp - 1, 0));
+      n_above += (warp > 0 ? wa : 0u) - above;
+      n_equal += (warp > 0 ? we : 0u) - equal;
+      if (CLUSTER) {
+        unit_barrier<CLUSTER>();
+        uint32_t ra = lane < rank ? peer_word(&sh.totals[0], lane) : 0u, re = lane < rank ? peer_word(&sh.totals[1], lane) : 0u;
+        n_above += __reduce_add_sync(0xffffffffu, ra);
+        n_equal += __reduce_add_sync(0xffffffffu, re);
+      }
+      if (above + equal > 0) {
+        for (int i = s0; i < s1; ++i) {
+          const uint32_t x = word(i);
+          if (x > prefix || (x == prefix && n_equal < need)) out[lo + n_above + min(n_equal, need)] = r0 + i;
+          n_above += x > prefix;
+          n_equal += x == prefix;
         }
       }
-      const uint32_t below = (1u << lane) - 1u;
-      for (int i0 = s0; i0 < s1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t x = i < s1 ? word(i) : 0u;
-        const bool up = i < s1 && x > prefix, tie = i < s1 && x == prefix;
-        const uint32_t ba = __ballot_sync(0xffffffffu, up), be = __ballot_sync(0xffffffffu, tie);
-        const uint32_t ties = n_equal + __popc(be & below);
-        if (up || (tie && ties < need))
-          out[lo + n_above + __popc(ba & below) + min(ties, need)] = r0 + i;
-        n_above += __popc(ba);
-        n_equal += __popc(be);
-      }
-      if (size > 1) cluster_barrier(size);  // no rank ends while another reads its counts
+      if (CLUSTER) unit_barrier<CLUSTER>();  // no rank ends while another reads its counts
     }
   }
-  if (p.gather_here) {
+  if (!CLUSTER && p.gather_here) {
     __syncthreads();
     gather_rows(p, sq, h, 0, sq.keep, p.row_bytes / 16, t, kSelThreads);
   }
@@ -259,17 +282,18 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
 }  // namespace
 
 cudaError_t launch_evict(EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s, int* launches) {
-  // one CTA for a few thousand tokens, else runs of about 4096 over a cluster
+  // one CTA up to 8192 tokens, else a cluster of runs of 4096 to 8192 while it grows
   int size = 1;
   while (size < kMaxCluster && max_len > 8192 * size) size *= 2;
   const int share = (max_len + size - 1) / size;
   const size_t smem = sizeof(SelShared) + (size_t)std::min(share, kCached) * sizeof(uint32_t);
   // up to 64 KB of rows a unit the choosing CTA copies them itself
   p.gather_here = size == 1 && (int64_t)max_keep * p.row_bytes <= 32 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto kernel = size > 1 ? evict_select_kernel<true> : evict_select_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(sizeof(SelShared) + kCached * sizeof(uint32_t)));
   if (e == cudaSuccess && size > 8)
-    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)size, (unsigned)p.Hkv, (unsigned)p.n_seqs);
@@ -284,7 +308,7 @@ cudaError_t launch_evict(EvictParams& p, int32_t max_len, int32_t max_keep, cuda
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = size > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   *launches = 1;
   if (e != cudaSuccess || p.gather_here) return e;
   const int rows = kPieces / (p.row_bytes / 16);

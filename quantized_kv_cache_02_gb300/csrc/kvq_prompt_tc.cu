@@ -76,8 +76,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int valid = sq.len - (nmax - 1) * kKeys;
   const bool clear = valid < kKeys && (valid & 15) != 0;
 
+  // the copies: Q_0, K_0, Q_1, then the pairs V_j, K_j+1
+  auto load_q = [&](int i) {
+    bar_expect(bar_q + 8 * i, (uint32_t)(tile_tok * p.g) * 128u * (D / 64));
+    for (int c = 0; c < D / 64; ++c)
+      tma_load3(sbase + L::kQ + i * L::kTile + c * L::kChunk, &maps.q, 64 * c, h * p.g, sq.start + tok0 + i * tile_tok,
+                bar_q + 8 * i);
+  };
+  auto load_kv = [&](const CUtensorMap* m, uint32_t dst, int blk, uint32_t bar) {
+    for (int c = 0; c < D / 64; ++c)
+      tma_load3(sbase + dst + c * L::kChunk, m, 64 * c, sq.start + blk * kKeys, h, bar);
+  };
+  auto load_pair = [&](int j) {
+    const int s = j % L::kSlots;
+    const bool more = j + 1 < nmax;
+    bar_expect(bar_full + 8 * s, L::kTile * (more ? 2 : 1));
+    load_kv(&maps.v, L::kRing + 2 * s * L::kTile, j, bar_full + 8 * s);
+    if (more) load_kv(&maps.k, L::kRing + (2 * s + 1) * L::kTile, j + 1, bar_full + 8 * s);
+  };
+
   if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
-  if (t == 0) {
+  if (t == 32 * kCopyWarp) {
+    // the first copies fly while the rest of the CTA sets up
     *abort = 0;
     for (int s = 0; s < L::kSlots; ++s) {
       bar_init(bar_full + 8 * s, 1);
@@ -93,6 +113,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bar_init(bar_o + 8 * i, 1);
     }
     bar_init_fence();
+    pdl_wait();
+    load_q(0);
+    bar_expect(bar_k0, L::kTile);
+    load_kv(&maps.k, L::kK0, 0, bar_k0);
+    if (n1 > 0) load_q(1);
+    for (int j = 0; j < min(nmax, L::kSlots); ++j) load_pair(j);
   }
   tm_fence_before();
   __syncthreads();
@@ -104,36 +130,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
-      // ============ copies (lane 0): Q_0, K_0, Q_1, then the pairs V_j, K_j+1 ========
-      int issued = 0;
+      // ============ copies (lane 0) ==================================================
+      int issued = min(nmax, L::kSlots);
       if (lane == 0) {
-        const uint32_t qbytes = (uint32_t)(tile_tok * p.g) * 128u * (D / 64);
-        auto load_q = [&](int i) {
-          bar_expect(bar_q + 8 * i, qbytes);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load3(sbase + L::kQ + i * L::kTile + c * L::kChunk, &maps.q, 64 * c, h * p.g,
-                      sq.start + tok0 + i * tile_tok, bar_q + 8 * i);
-        };
-        auto load_kv = [&](const CUtensorMap* m, uint32_t dst, int blk, uint32_t bar) {
-          for (int c = 0; c < D / 64; ++c)
-            tma_load3(sbase + dst + c * L::kChunk, m, 64 * c, sq.start + blk * kKeys, h, bar);
-        };
-        load_q(0);
-        bar_expect(bar_k0, L::kTile);
-        load_kv(&maps.k, L::kK0, 0, bar_k0);
-        if (n1 > 0) load_q(1);
-        for (int j = 0; j < nmax; ++j) {
-          const int s = j % L::kSlots;
-          if (j >= L::kSlots && !bar_wait(bar_empty + 8 * s, (uint32_t)(j / L::kSlots - 1) & 1u, abort)) {
+        for (; issued < nmax; ++issued) {
+          if (!bar_wait(bar_empty + 8 * (issued % L::kSlots), (uint32_t)(issued / L::kSlots - 1) & 1u, abort)) {
             *abort = 1;
             if (p.status) atomicOr(p.status, kStatusPromptTimeout);
             break;
           }
-          const bool more = j + 1 < nmax;
-          bar_expect(bar_full + 8 * s, L::kTile * (more ? 2 : 1));
-          load_kv(&maps.v, L::kRing + 2 * s * L::kTile, j, bar_full + 8 * s);
-          if (more) load_kv(&maps.k, L::kRing + (2 * s + 1) * L::kTile, j + 1, bar_full + 8 * s);
-          ++issued;
+          load_pair(issued);
         }
       }
       issued = __shfl_sync(0xffffffffu, issued, 0);
@@ -312,18 +318,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int head = h * p.g + r - tt * p.g;
       __nv_bfloat16* dst =
           static_cast<__nv_bfloat16*>(p.out) + (int64_t)(sq.start + pos) * p.o_ts + (int64_t)head * p.o_hs;
+      // through the tile's Q buffer (no MMA reads it any more), 16-byte pieces
+      // swizzled by row, so that the warp stores whole rows: one row a thread
+      // took a memory transaction a piece, 2 us a CTA
+      constexpr int kPieces = D / 8;
+      uint8_t* stage = smem + L::kQ + i * L::kTile + (warp & 3) * 32 * (2 * D);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
         tm_ld32(to + 32 * c, o);
         tm_wait_ld();
-        if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(dst + 32 * c + e) =
-                make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                           pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-        }
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4*>(stage + lane * (2 * D) + ((4 * c + e / 8) ^ (lane & (kPieces - 1))) * 16) =
+              make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                         pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+      }
+      __syncwarp();
+      const uint32_t rows_live = __ballot_sync(0xffffffffu, live);
+#pragma unroll 4
+      for (int x = lane; x < 32 * kPieces; x += 32) {
+        const int row = x / kPieces, c = x % kPieces;
+        const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + row * (2 * D) + (c ^ (row & (kPieces - 1))) * 16);
+        if (rows_live >> row & 1u) *reinterpret_cast<uint4*>(at + 16 * c) = v;
       }
       if (live && p.lse)
         p.lse[(int64_t)head * p.n_tokens + sq.start + pos] = (m + log2f(l)) * 0.69314718055994530942f;

@@ -91,8 +91,27 @@ __global__ void __launch_bounds__(kWThreads, 1)
     return (resident || key < tok0 ? 0 : (key - tok0) / tile_tok) + rank;
   };
 
+  // the copies: key pairs and query tiles
+  auto load_pair = [&](int pr) {
+    const int s = pr & 1, key = run0 + pr * 2 * kKeys, both = key + kKeys < sq.len;
+    bar_expect(bar_kf + 8 * s, L::kTile * (both ? 2 : 1));
+    for (int w = 0; w < 1 + both; ++w)
+      for (int c = 0; c < D / 64; ++c)
+        tma_load3(sbase + k_tile(pr, w) + c * L::kChunk, &maps.k, 64 * c, sq.start + key + w * kKeys, h, bar_kf + 8 * s);
+  };
+  auto load_q = [&](int i, int s) {
+    bar_expect(bar_qf + 8 * s, (uint32_t)(tile_tok * p.g) * 128u * (D / 64));
+    for (int c = 0; c < D / 64; ++c)
+      tma_load3(sbase + q_tile(s) + c * L::kChunk, &maps.q, 64 * c, h * p.g, sq.start + tok0 + i * tile_tok,
+                bar_qf + 8 * s);
+  };
+  // those that wait for nothing: the first pair's query tiles that have a stage, and the pairs that have a place
+  const int q_early = max(0, min(kQStages, (nq - q_first(0) + p.split - 1) / p.split));
+  const int k_early = min(pairs, resident ? 2 : 1);
+
   if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
-  if (t == 0) {
+  if (t == 32 * kCopyWarp) {
+    // they fly while the rest of the CTA sets up
     *abort = 0;
     for (int i = 0; i < 2; ++i) {
       bar_init(bar_kf + 8 * i, 1);
@@ -107,6 +126,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       bar_init(bar_se + 8 * i, 128);
     }
     bar_init_fence();
+    pdl_wait();
+    for (int pr = 0; pr < k_early; ++pr) load_pair(pr);
+    for (int x = 0; x < q_early; ++x) load_q(q_first(0) + x * p.split, x);
   }
   if (t < 256) {
     *reinterpret_cast<uint4*>(smem + L::kOnes + t * 16) =
@@ -126,11 +148,6 @@ __global__ void __launch_bounds__(kWThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
       // ============ copies; the lanes turn lse into -L =================================
-      if (lane == 0) {
-        tma_prefetch(&maps.q);
-        tma_prefetch(&maps.k);
-      }
-      const uint32_t qbytes = (uint32_t)(tile_tok * p.g) * 128u * (D / 64);
       auto row_lse = [&](int i, int r) -> float {
         const int tt = r / p.g, pos = tok0 + i * tile_tok + tt;
         return tt < tile_tok && pos < sq.len
@@ -144,22 +161,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
         for (int e = 0; e < 4; ++e) ahead[e] = row_lse(i, 32 * e + lane);
         ahead_tile = i;
       };
-      int issued = 0, kpairs = 0;
+      int issued = 0;
       bool go = true;
-      auto load_q = [&](int i, int then) {  // tile i; its successor's lse is fetched under it
-        const int s = issued % kQStages, round = issued / kQStages;
+      auto give_q = [&](int i, int then) {  // tile i; its successor's lse is fetched under it
+        const int s = issued % kQStages;
+        if (issued >= q_early) {
+          if (!(go = warp_wait(bar_qe + 8 * s, (uint32_t)(issued / kQStages - 1) & 1u, abort))) return;
+          if (lane == 0) load_q(i, s);
+        }
         if (ahead_tile != i) fetch_lse(i);
         float now[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) now[e] = ahead[e];
         if (then >= 0) fetch_lse(then);
-        if (round > 0 && !(go = warp_wait(bar_qe + 8 * s, (uint32_t)(round - 1) & 1u, abort))) return;
-        if (lane == 0) {
-          bar_expect(bar_qf + 8 * s, qbytes);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load3(sbase + q_tile(s) + c * L::kChunk, &maps.q, 64 * c, h * p.g,
-                      sq.start + tok0 + i * tile_tok, bar_qf + 8 * s);
-        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           // -L = -lse * lse_hi - lse * lse_lo, cut into four pieces of 8 bits
@@ -174,24 +188,20 @@ __global__ void __launch_bounds__(kWThreads, 1)
         bar_arrive(bar_qf + 8 * s);
         ++issued;
       };
+      int kpairs = k_early;
       for (int pr = 0; pr < pairs && go; ++pr) {
-        const int s = pr & 1;
-        if (pr > 1 && !(go = warp_wait(bar_ke + 8 * s, (uint32_t)(pr / 2 - 1) & 1u, abort))) break;
-        const int key = run0 + pr * 2 * kKeys, both = key + kKeys < sq.len;
-        if (lane == 0) {
-          bar_expect(bar_kf + 8 * s, L::kTile * (both ? 2 : 1));
-          for (int w = 0; w < 1 + both; ++w)
-            for (int c = 0; c < D / 64; ++c)
-              tma_load3(sbase + k_tile(pr, w) + c * L::kChunk, &maps.k, 64 * c,
-                        sq.start + key + w * kKeys, h, bar_kf + 8 * s);
+        if (pr >= k_early) {
+          if (!(go = warp_wait(bar_ke + 8 * (pr & 1), (uint32_t)(pr / 2 - 1) & 1u, abort))) break;
+          if (lane == 0) load_pair(pr);
+          ++kpairs;
         }
-        ++kpairs;
         if (pr == 0 || !resident)
-          for (int i = q_first(pr); i < nq && go; i += p.split) load_q(i, i + p.split < nq ? i + p.split : -1);
+          for (int i = q_first(pr); i < nq && go; i += p.split) give_q(i, i + p.split < nq ? i + p.split : -1);
       }
       if (!go) {
         *abort = 1;
         if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
+        for (; issued < q_early; ++issued) bar_arrive(bar_qf + 8 * issued);  // complete but for the copy
       }
       // nothing in flight when the CTA ends
       for (int x = max(0, kpairs - 2); x < kpairs; ++x) bar_drain(bar_kf + 8 * (x & 1), (uint32_t)(x / 2) & 1u);
