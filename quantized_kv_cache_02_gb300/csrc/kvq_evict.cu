@@ -8,16 +8,17 @@
 // order-preserving words.  A radix select finds the left-th largest word eight
 // bits at a time (each CTA counts its run, all add up every CTA's 256 counts
 // through distributed shared memory: one cluster barrier a pass); one ordered
-// pass then writes the kept tokens.  Every weight is read once.  With 256
-// counters two CTAs of 27,000 words fit an SM and eight units of 432,000 tokens
-// run at once: SELTIME; passes of 11 bits, whose 2048 counters read
-// from 16 peers took 10 us a pass and whose clusters came in two waves, 163 us.
+// pass then writes the kept tokens.  Every weight is read once.  Eight
+// units of 432,000 tokens take 34 us as clusters of 12 that run at once; of 16 (two waves, or two
+// CTAs an SM) 56 and 41 us, and passes of 11 bits, whose 2048 counters are read from
+// every peer, 163 us.
 //
 // Gather.  A thread has four 16-byte pieces of K and of V in flight.  Bound by
 // HBM: 16 bytes a kept piece read and written.  Small choices gather in the
 // choosing CTA and save the second launch.
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_prompt.h"
 
@@ -43,7 +44,8 @@ struct SelShared {
   uint32_t totals[2];                           // of the CTA
   uint32_t digit, rank;
 };
-static_assert(sizeof(SelShared) + kCached * sizeof(uint32_t) <= 227 * 1024, "a run has to fit shared memory");
+constexpr int kSelSmemMax = (int)(sizeof(SelShared) + kCached * sizeof(uint32_t));
+static_assert(kSelSmemMax <= 227 * 1024, "a run has to fit shared memory");
 
 template <bool CLUSTER>
 __device__ __forceinline__ void unit_barrier() {
@@ -106,9 +108,9 @@ __device__ __forceinline__ void gather_rows(const EvictParams& p, const EvictSeq
   }
 }
 
-// CLUSTER: a cluster a unit, two CTAs an SM; else one CTA, which may also copy the rows.
+// CLUSTER: a cluster a unit; else one CTA, which may also copy the rows.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads, CLUSTER ? 2 : 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint8_t sel_smem[];
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_smem);
   uint32_t* run = reinterpret_cast<uint32_t*>(sel_smem + sizeof(SelShared));
@@ -281,19 +283,52 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
 
 }  // namespace
 
+// Clusters of ``size`` choosing CTAs that run at once with one CTA an SM; asked
+// of the driver once a device and size.
+static int active_clusters(int size) {
+  static std::atomic<int> known[64][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][size].load();
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kSelSmemMax;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev][size].store(n);
+  return n;
+}
+
 cudaError_t launch_evict(EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s, int* launches) {
-  // one CTA up to 8192 tokens, else a cluster of runs of 4096 to 8192 while it grows
+  // the largest cluster that leaves each CTA 4096 tokens and lets every unit run
+  // at once; more units than that fill the GPU with one CTA each
   int size = 1;
-  while (size < kMaxCluster && max_len > 8192 * size) size *= 2;
+  const int64_t units = (int64_t)p.Hkv * p.n_seqs;
+  if (max_len >= 8192) {
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    for (int c : {2, 4, 8, 12, 16})
+      if ((int64_t)c * 4096 <= max_len && units <= active_clusters(c)) size = c;
+  }
   const int share = (max_len + size - 1) / size;
   const size_t smem = sizeof(SelShared) + (size_t)std::min(share, kCached) * sizeof(uint32_t);
   // up to 64 KB of rows a unit the choosing CTA copies them itself
   p.gather_here = size == 1 && (int64_t)max_keep * p.row_bytes <= 32 * 1024;
   const auto kernel = size > 1 ? evict_select_kernel<true> : evict_select_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(SelShared) + kCached * sizeof(uint32_t)));
-  if (e == cudaSuccess && size > 8)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cudaError_t e = cudaSuccess;
+  if (size == 1) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)size, (unsigned)p.Hkv, (unsigned)p.n_seqs);

@@ -104,12 +104,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bar_init(bar_empty + 8 * s, 1);
     }
     bar_init(bar_k0, 1);
-    bar_init(bar_clear, 32);
+    bar_init(bar_clear, 1);
     for (int i = 0; i < 2; ++i) {
       bar_init(bar_q + 8 * i, 1);
       bar_init(bar_s + 8 * i, 1);
-      bar_init(bar_p + 16 * i, 128);
-      bar_init(bar_p + 16 * i + 8, 128);
+      bar_init(bar_p + 16 * i, 4);  // a warp arrives once, by one lane
+      bar_init(bar_p + 16 * i + 8, 4);
       bar_init(bar_o + 8 * i, 1);
     }
     bar_init_fence();
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *reinterpret_cast<uint4*>(v + c * L::kChunk + valid * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         async_proxy_fence();
-        bar_arrive(bar_clear);
+        warp_arrive(bar_clear);
       }
       bar_drain(bar_k0, 0);
       bar_drain(bar_q, 0);
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (c == 32) {  // the first 64 keys' weights: their P V may start
             tm_wait_st();
             tm_fence_before();
-            bar_arrive(bar_p + 16 * i);
+            warp_arrive(bar_p + 16 * i);
           }
         }
         sum[0] = add2(sum[0], sum[1]);
@@ -304,9 +304,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_wait_st();
         tm_fence_before();
       } else {
-        bar_arrive(bar_p + 16 * i);
+        warp_arrive(bar_p + 16 * i);
       }
-      bar_arrive(bar_p + 16 * i + 8);
+      warp_arrive(bar_p + 16 * i + 8);
     }
     if (ok && n > 0) ok = warp_wait(bar_o + 8 * i, 0, abort);
     if (!ok) {

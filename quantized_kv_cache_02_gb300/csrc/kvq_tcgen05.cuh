@@ -47,6 +47,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const vo
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
 }
+// One arrival for the warp, once every lane is here: arrivals on one barrier are
+// taken one after the other, 128 of them some 500 cycles.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+}
 // A wait that is not cut short: for copies and MMAs in flight when a CTA stops.
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
   for (uint32_t it = 0; it < kBarTries; ++it)

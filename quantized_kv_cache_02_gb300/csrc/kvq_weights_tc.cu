@@ -10,13 +10,16 @@
 //
 // so a thread owns one key and its sum never leaves a register.  A CTA takes
 // pairs of key tiles: warps 0-3 sum the first, warps 4-7 the second, and both
-// use every query tile that arrives.  Each key tile has two score buffers, so
-// MMAs and exponentials overlap.  With few counted queries (at most two tiles)
-// the query tiles stay in shared memory and a run of pairs streams past them;
-// else a CTA has one pair, which stays while the queries stream.
-// ``split`` CTAs of a cluster take a pair's query tiles in turn and rank 0 adds
-// their sums in rank order, so a short prompt fills the GPU and the result
-// has the same bits every time.
+// use every query tile that arrives.  Those threads also put the Keys into tensor
+// memory, one row each: with K and Q both read from shared memory the MMAs
+// took all of its bandwidth and every barrier waited for it (80 us for 4096 whole
+// tokens, 32/8 heads of 128, against NEWTIME).  Three score buffers, which
+// the two tiles take in turn, let MMAs and exponentials overlap.  With few
+// counted queries (at most two tiles) the query tiles stay in shared memory
+// and a run of pairs streams past them; else a CTA has one pair, which stays
+// while the queries stream.  ``split`` CTAs of a cluster take a pair's query
+// tiles in turn and rank 0 adds their sums in rank order, so a short prompt
+// fills the GPU and the result has the same bits every time.
 //
 // The row's L_r enters in the MMA: one more k-step of 16 takes it off every
 // score, as four bf16 pieces against a column of ones, so an element costs one
@@ -38,7 +41,7 @@ namespace {
 constexpr int kKeys = 128, kRows = 128;
 constexpr int kMmaWarp = 8, kCopyWarp = 9, kWThreads = 384;  // warps 10 and 11 only fill the third warpgroup
 constexpr int kSumRegs = 200, kOtherRegs = 104;              // a thread, out of the launch's 3 x 168
-constexpr int kQStages = 4, kStayTiles = 2;
+constexpr int kQStages = 4, kStayTiles = 2, kSBuffers = 3;
 
 template <int D>
 struct WLayout {
@@ -51,8 +54,10 @@ struct WLayout {
   static constexpr uint32_t kL = kStay + 2 * kTile, kOnes = kL + kQStages * 2048, kZero = kOnes + 2048;
   static constexpr uint32_t kRed = kZero + 2048;                 // [8 ranks][256 keys]
   static constexpr uint32_t kBars = kRed + 8 * 256 * 4;
-  // K full / empty (2 each), Q full / empty, S full / empty (tile, buffer)
-  static constexpr int kNBars = 4 + 2 * kQStages + 8;
+  // K full / empty (2 each), K in tensor memory, Q full / empty, S full / empty
+  static constexpr int kNBars = 5 + 2 * kQStages + 2 * kSBuffers;
+  // tensor memory: key tile w at 64 w, score buffer b at 128 + 128 b
+  static constexpr uint32_t kColS = 128;
   static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;
 };
 
@@ -68,8 +73,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint8_t* smem = w_raw + ((1024u - (smem_u32(w_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t bar_kf = sbase + L::kBars, bar_ke = bar_kf + 16, bar_qf = bar_ke + 16,
-                 bar_qe = bar_qf + 8 * kQStages, bar_sf = bar_qe + 8 * kQStages, bar_se = bar_sf + 32;
+  const uint32_t bar_kf = sbase + L::kBars, bar_ke = bar_kf + 16, bar_kt = bar_ke + 16, bar_qf = bar_kt + 8,
+                 bar_qe = bar_qf + 8 * kQStages, bar_sf = bar_qe + 8 * kQStages, bar_se = bar_sf + 8 * kSBuffers;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
 
@@ -115,15 +120,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
     *abort = 0;
     for (int i = 0; i < 2; ++i) {
       bar_init(bar_kf + 8 * i, 1);
-      bar_init(bar_ke + 8 * i, 1);
+      bar_init(bar_ke + 8 * i, 8);  // a warp arrives once, by one lane
     }
+    bar_init(bar_kt, 8);
     for (int i = 0; i < kQStages; ++i) {
-      bar_init(bar_qf + 8 * i, 1 + 32);  // the copy, and the lanes that wrote -L
+      bar_init(bar_qf + 8 * i, 2);  // the copy, and the warp that wrote -L
       bar_init(bar_qe + 8 * i, 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kSBuffers; ++i) {
       bar_init(bar_sf + 8 * i, 1);
-      bar_init(bar_se + 8 * i, 128);
+      bar_init(bar_se + 8 * i, 4);
     }
     bar_init_fence();
     pdl_wait();
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
               make_uint4(pack_bf16(b0, b1), pack_bf16(b2, last - b2), 0u, 0u);
         }
         async_proxy_fence();
-        bar_arrive(bar_qf + 8 * s);
+        warp_arrive(bar_qf + 8 * s);
         ++issued;
       };
       int kpairs = k_early;
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (!go) {
         *abort = 1;
         if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
-        for (; issued < q_early; ++issued) bar_arrive(bar_qf + 8 * issued);  // complete but for the copy
+        for (; issued < q_early; ++issued) warp_arrive(bar_qf + 8 * issued);  // complete but for the copy
       }
       // nothing in flight when the CTA ends
       for (int x = max(0, kpairs - 2); x < kpairs; ++x) bar_drain(bar_kf + 8 * (x & 1), (uint32_t)(x / 2) & 1u);
@@ -211,45 +217,41 @@ __global__ void __launch_bounds__(kWThreads, 1)
       // ============ MMAs, all issued by one lane ========================================
       const bool one = elect_one();
       constexpr uint32_t idesc = bf16_idesc(kKeys, kRows, false);
-      int taken = 0, n_s[2] = {0, 0};
+      int taken = 0, n_s = 0;
       bool ok = true;
       for (int pr = 0; pr < pairs && ok; ++pr) {
         const int both = run0 + pr * 2 * kKeys + kKeys < sq.len;
-        ok = bar_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort);
+        ok = bar_wait(bar_kt, (uint32_t)pr & 1u, abort);
         for (int i = q_first(pr); i < nq && ok; i += p.split) {
           const int s = resident ? i : taken % kQStages;
           ok = bar_wait(bar_qf + 8 * s, resident ? 0u : (uint32_t)(taken / kQStages) & 1u, abort);
           ++taken;
+          const uint64_t db = sw128_desc(sbase + q_tile(s), 0);
           for (int w = 0; w < 1 + both && ok; ++w) {
-            const int b = 2 * w + (n_s[w] & 1);
-            if (n_s[w] > 1) ok = bar_wait(bar_se + 8 * b, (uint32_t)(n_s[w] / 2 - 1) & 1u, abort);
+            const int b = n_s % kSBuffers;
+            if (n_s >= kSBuffers) ok = bar_wait(bar_se + 8 * b, (uint32_t)(n_s / kSBuffers - 1) & 1u, abort);
             if (!ok) break;
             tm_fence_after();
-            const uint64_t da = sw128_desc(sbase + k_tile(pr, w), 0);
-            const uint64_t db = sw128_desc(sbase + q_tile(s), 0);
+            const uint32_t d = tm + L::kColS + 128 * b;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
-              if (one) mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > 0);
-            }
+            for (int ks = 0; ks < D / 16; ++ks)
+              if (one) mma_ts(d, tm + 64 * w + 8 * ks, db + (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2, idesc, ks > 0);
             if (one) {
-              mma_ss(tm + 128 * b, plain_desc(sbase + L::kOnes, 2048),
+              mma_ss(d, plain_desc(sbase + L::kOnes, 2048),
                      plain_desc(sbase + L::kL + s * 2048, L::kZero - L::kL - s * 2048), idesc, 1);
               mma_commit(bar_sf + 8 * b);
             }
-            ++n_s[w];
+            ++n_s;
           }
           if (one && !resident) mma_commit(bar_qe + 8 * s);
         }
-        if (one) mma_commit(bar_ke + 8 * (pr & 1));
       }
       if (!ok) {
         *abort = 1;
         if (one && p.status) atomicOr(p.status, kStatusPromptTimeout);
       }
-      // nothing in flight when the CTA ends: the last commit on a score buffer covers the MMAs before it
-      for (int w = 0; w < 2; ++w)
-        for (int x = max(0, n_s[w] - 2); x < n_s[w]; ++x) bar_drain(bar_sf + 8 * (2 * w + (x & 1)), (uint32_t)(x / 2) & 1u);
+      // nothing in flight when the CTA ends: the last commit covers the MMAs before it
+      if (n_s > 0) bar_drain(bar_sf + 8 * ((n_s - 1) % kSBuffers), (uint32_t)((n_s - 1) / kSBuffers) & 1u);
     }
   } else {
     // ============ sums: key tile w, one key a thread ==================================
@@ -257,22 +259,43 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int w = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float2 sc = make_float2(p.scale2, p.scale2);
-    int n_s = 0;
+    int n_s = 0;  // score tiles of the CTA before this pair's
     bool ok = true;
     for (int pr = 0; pr < pairs && ok; ++pr) {
       const int tile_key = run0 + pr * 2 * kKeys + w * kKeys, key = tile_key + (t & 127);
       const bool active = tile_key < sq.len;
+      const int tiles = run0 + pr * 2 * kKeys + kKeys < sq.len ? 2 : 1;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      for (int i = q_first(pr); i < nq && active; i += p.split) {
-        const int b = 2 * w + (n_s & 1);
-        if (!(ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n_s / 2) & 1u, abort))) break;
-        ++n_s;
+      // this key's row into tensor memory (the last pair's MMAs are done: their scores were)
+      if (!(ok = warp_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort))) break;
+      if (active) {
+        const uint8_t* row = smem + k_tile(pr, w) + (t & 127) * 128;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {  // 32 channels: four 16-byte pieces, swizzled by row
+          uint32_t x[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(x + 4 * e) = *reinterpret_cast<const uint4*>(
+                row + (c / 2) * L::kChunk + (((c & 1) * 4 + e) ^ (t & 7)) * 16);
+          tm_st16(tm + 64 * w + 16 * c + lanes, x);
+        }
+        tm_wait_st();
+        tm_fence_before();
+      }
+      warp_arrive(bar_ke + 8 * (pr & 1));
+      warp_arrive(bar_kt);
+      int n = n_s + w;
+      for (int i = q_first(pr); i < nq; i += p.split, n += tiles) {
+        n_s += tiles;
+        if (!active) continue;
+        const int b = n % kSBuffers;
+        if (!(ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n / kSBuffers) & 1u, abort))) break;
         tm_fence_after();
         // rows [lo, hi) of the tile count for this key
         const int pos0 = tok0 + i * tile_tok;
         const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
-        const uint32_t ts = tm + 128 * b + lanes;
+        const uint32_t ts = tm + L::kColS + 128 * b + lanes;
         auto add_tile = [&](auto with_mask) {
           float x[2][32];
           tm_ld32(ts, x[0]);
@@ -297,7 +320,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (masked) add_tile(std::true_type());
         else add_tile(std::false_type());
         tm_fence_before();
-        bar_arrive(bar_se + 8 * b);
+        warp_arrive(bar_se + 8 * b);
       }
       if (!ok) break;
       sum[0] = add2(sum[0], sum[1]);
