@@ -59,7 +59,7 @@ struct PromptParams {
   int64_t n_tokens;
   int64_t last;                // weights: queries counted back from each sequence's end
   float lse_hi, lse_lo;        // weights: lse times their sum is in the scores' units
-  int32_t split;               // weights on the tensor cores: CTAs that share a pair of key tiles
+  int32_t split;               // CTAs of a cluster that share a tile (of queries, or a pair of key tiles)
   int32_t* status;
   PromptTiles tiles;
 };
@@ -85,8 +85,30 @@ struct EvictParams {
   EvictSeq seq[kMaxSeqsPerLaunch];
 };
 
+// Launch with clusters of ``split`` CTAs in a row a tile.
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), int64_t tiles, int split, int threads, size_t smem, cudaStream_t s,
+                           const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Launchers (return the launch's error code).
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
+// CTAs that share a tile of the CUDA-core attention
+int prompt_simt_split(int64_t tiles, int32_t max_len, int n_sm);
 cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
 cudaError_t launch_evict(EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s, int* launches);
 

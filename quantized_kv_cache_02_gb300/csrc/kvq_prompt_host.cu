@@ -228,12 +228,15 @@ kvq_status prompt_attention(const kvq_prompt* p, const void* q, const void* k, c
   pp.lse = lse;
   const bool tc = tensor_cores(p);
   const int step = tc ? kvq::prompt_tc_tokens(pp.g) : kvq::kPromptRows / pp.g;
+  int n_sm = 0;
+  KVQ_TRY(sm_count(&n_sm));
   const auto launches = launches_of(p);
   for (const auto& l : launches)
-    if (fill_tiles(l, pp.Hkv, step, &pp.tiles) > kMaxTiles) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
+    if (fill_tiles(l, pp.Hkv, step, &pp.tiles) > kMaxTiles / 4) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
   for (const auto& l : launches) {
     const int64_t tiles = fill_tiles(l, pp.Hkv, step, &pp.tiles);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    pp.split = tc ? 1 : kvq::prompt_simt_split(tiles, l[0].len, n_sm);
     const cudaError_t e = tc ? kvq::launch_prompt_tc(pp, tiles, s)
                              : kvq::launch_prompt_simt(pp, p->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
     if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");

@@ -12,12 +12,19 @@
 //               attn_full in section 04's appendix, softmax(QK^T / sqrt(d) + M) V)
 //   weights:    w_j = sum over the last queries i >= j of 2^(s_ij - lse_i)
 //
-// Bound: FMA issue.  Per four channels a thread does 64 FMAs for 8 16-byte
-// shared loads (12 wavefronts a warp against 16 cycles of FMA).
+// Bound: the FMA pipe.  Products run as packed pairs (two channels of a score,
+// two columns of the output): the pipe's rate is the same, but half the issue
+// slots stay free for the shared loads (per four channels 12 wavefronts and 40
+// instructions a warp against 64 cycles of FMA).  Few tiles are split along
+// the keys over a cluster (``split`` CTAs take the key steps in turn) and joined
+// through distributed shared memory in rank order; a causal prompt's last tiles
+// are otherwise what everything waits for.  1999 fp32 tokens, 8/2 heads of 128:
+// NEWFP32 us, 286 us without either.
 
 #include <cuda_bf16.h>
 
 #include "kvq_prompt.h"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 namespace {
@@ -68,10 +75,11 @@ __device__ __forceinline__ void load_queries(float* dst, int stride, const Promp
 
 __device__ __forceinline__ void scores(float (&s)[4][4], const float* qs, const float* ks, int stride, int D, int ty,
                                        int tx) {
+  float2 acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int c = 0; c < D; c += 4) {
     float4 a[4], b[4];
@@ -83,24 +91,50 @@ __device__ __forceinline__ void scores(float (&s)[4][4], const float* qs, const 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        acc[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), acc[i][j]);
+        acc[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), acc[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = acc[i][j].x + acc[i][j].y;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 peer_load4(const float* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_addr(p, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 peer_load2(const float2* p, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_addr(p, rank)) : "memory");
+  return v;
 }
 
 // NC: 64-channel column groups of the output (D <= 64 NC).
 template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(const __grid_constant__ PromptParams p) {
   extern __shared__ __align__(16) float simt_smem[];
   constexpr int kStride = 64 * NC + 4;
   float* qs = simt_smem;                        // [64][kStride]
   float* ks = qs + kPromptRows * kStride;       // K, then V
   float* ps = ks + kPromptKeys * kStride;       // [64][kPStride]
   int si, h, level;
-  prompt_tile(p.tiles, blockIdx.x, &si, &h, &level);
+  const int rank = blockIdx.x % p.split;  // clusters are ``split`` CTAs in a row
+  prompt_tile(p.tiles, blockIdx.x / p.split, &si, &h, &level);
   const PromptSeq sq = p.tiles.seq[si];
   const int tile_tok = p.tiles.step, tok0 = level * tile_tok;
   const T* q = static_cast<const T*>(p.q) + (int64_t)sq.start * p.q_ts;
@@ -111,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
   pdl_release();
   load_queries(qs, kStride, p, q, tok0, tile_tok, sq.len, h);
   const int end = min(sq.len, tok0 + tile_tok);  // keys some row sees
-  float o[NC][4][4], m[4], l[4];
+  float2 o[NC][4][2];
+  float m[4], l[4];
   int pos[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -119,11 +154,9 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[c][i][j] = 0.f;
+    for (int c = 0; c < NC; ++c) o[c][i][0] = o[c][i][1] = make_float2(0.f, 0.f);
   }
-  for (int k0 = 0; k0 < end; k0 += kPromptKeys) {
+  for (int k0 = rank * kPromptKeys; k0 < end; k0 += p.split * kPromptKeys) {
     __syncthreads();  // the previous step's V has been read
     load_keys(ks, kStride, p.D, k, p.k_ts, k0, end, p.D);
     __syncthreads();
@@ -140,22 +173,23 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
       }
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-      // key 0 is in every row's first step, so the maximum is finite from then on
-      const float mn = fmaxf(m[i], mx), a = exp2f(m[i] - mn);
+      // (a row may see none of a later rank's keys)
+      const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn, a = exp2f(m[i] - base);
       m[i] = mn;
       float sum = 0.f;
       float* row = ps + (4 * ty + i) * kPStride;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float e = exp2f(s[i][j] - mn);
+        const float e = exp2f(s[i][j] - base);
         sum += e;
         row[tx + 16 * j] = e;
       }
       l[i] = fmaf(l[i], a, sum);
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[c][i][j] *= a;
+      for (int c = 0; c < NC; ++c) {
+        o[c][i][0] = mul2(o[c][i][0], make_float2(a, a));
+        o[c][i][1] = mul2(o[c][i][1], make_float2(a, a));
+      }
     }
     __syncthreads();  // K has been read; P is complete
     load_keys(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D);
@@ -173,10 +207,8 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float pp = nn == 0 ? pr[i].x : nn == 1 ? pr[i].y : nn == 2 ? pr[i].z : pr[i].w;
-            o[c][i][0] = fmaf(pp, vv.x, o[c][i][0]);
-            o[c][i][1] = fmaf(pp, vv.y, o[c][i][1]);
-            o[c][i][2] = fmaf(pp, vv.z, o[c][i][2]);
-            o[c][i][3] = fmaf(pp, vv.w, o[c][i][3]);
+            o[c][i][0] = fma2(make_float2(pp, pp), make_float2(vv.x, vv.y), o[c][i][0]);
+            o[c][i][1] = fma2(make_float2(pp, pp), make_float2(vv.z, vv.w), o[c][i][1]);
           }
         }
       }
@@ -184,22 +216,59 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i, t = r / p.g, head = h * p.g + r - t * p.g;
-    float lt = l[i];
 #pragma unroll
-    for (int w = 8; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
-    if (t >= tile_tok || tok0 + t >= sq.len) continue;
-    const float inv = 1.f / lt;
-    T* dst = static_cast<T*>(p.out) + (int64_t)(sq.start + tok0 + t) * p.o_ts + (int64_t)head * p.o_hs;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = 64 * c + 4 * tx;
-      if (col < p.D)
-        store4(dst + col, make_float4(o[c][i][0] * inv, o[c][i][1] * inv, o[c][i][2] * inv, o[c][i][3] * inv));
-    }
-    if (p.lse && tx == 0)
-      p.lse[(int64_t)head * p.n_tokens + sq.start + tok0 + t] = (m[i] + log2f(lt)) * 0.69314718055994530942f;
+    for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
   }
+  auto finish = [&](int r, int col, float4 sum, float mr, float lr, bool first) {  // row r, columns col .. col + 3
+    const int t = r / p.g, head = h * p.g + r - t * p.g;
+    if (t >= tile_tok || tok0 + t >= sq.len) return;
+    const float inv = 1.f / lr;
+    T* dst = static_cast<T*>(p.out) + (int64_t)(sq.start + tok0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+    if (col < p.D) store4(dst + col, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+    if (p.lse && first)
+      p.lse[(int64_t)head * p.n_tokens + sq.start + tok0 + t] = (mr + log2f(lr)) * 0.69314718055994530942f;
+  };
+  if (p.split == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        finish(4 * ty + i, 64 * c + 4 * tx, make_float4(o[c][i][0].x, o[c][i][0].y, o[c][i][1].x, o[c][i][1].y), m[i],
+               l[i], c == 0 && tx == 0);
+    return;
+  }
+  // the ranks' partials meet: each puts its own in its shared memory, and joins its share of the rows
+  __syncthreads();  // V has been read
+  float2* ml = reinterpret_cast<float2*>(ps);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (tx == 0) ml[4 * ty + i] = make_float2(m[i], l[i]);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      *reinterpret_cast<float4*>(ks + (4 * ty + i) * kStride + 64 * c + 4 * tx) =
+          make_float4(o[c][i][0].x, o[c][i][0].y, o[c][i][1].x, o[c][i][1].y);
+  }
+  cluster_sync();
+  const int rows = kPromptRows / p.split;
+  for (int x = threadIdx.x; x < rows * 16 * NC; x += kThreads) {
+    const int r = rank * rows + x / (16 * NC), col = 4 * (x % (16 * NC));
+    float top = -INFINITY;
+    for (int k = 0; k < p.split; ++k) top = fmaxf(top, peer_load2(ml + r, k).x);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lr = 0.f;
+    for (int k = 0; k < p.split; ++k) {
+      const float2 part = peer_load2(ml + r, k);
+      const float4 v = peer_load4(ks + r * kStride + col, k);
+      const float a = exp2f(part.x - top);  // rank 0 holds key 0: top is finite
+      lr = fmaf(part.y, a, lr);
+      sum.x = fmaf(v.x, a, sum.x);
+      sum.y = fmaf(v.y, a, sum.y);
+      sum.z = fmaf(v.z, a, sum.z);
+      sum.w = fmaf(v.w, a, sum.w);
+    }
+    finish(r, col, sum, top, lr, col == 0);
+  }
+  cluster_sync();  // no rank ends while another reads its partials
 }
 
 // One CTA per 64 keys of a KV head: the column sums stay in registers while
@@ -260,7 +329,7 @@ template <typename K>
 cudaError_t launch_sized(K kernel, size_t smem, int64_t tiles, const PromptParams& p, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)tiles), dim3(kThreads), smem, s, p);
+  return launch_cluster(kernel, tiles, p.split, kThreads, smem, s, p);
 }
 
 template <typename T>
@@ -274,6 +343,12 @@ cudaError_t launch_attention_t(const PromptParams& p, int64_t tiles, cudaStream_
 }
 
 }  // namespace
+
+int prompt_simt_split(int64_t tiles, int32_t max_len, int n_sm) {
+  int split = 1;
+  while (split < 4 && tiles * split < 3 * (int64_t)n_sm && max_len >= 8 * split * kPromptKeys) split *= 2;
+  return split;
+}
 
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s) {
   return dtype == 0 ? launch_attention_t<__nv_bfloat16>(p, tiles, s) : launch_attention_t<float>(p, tiles, s);

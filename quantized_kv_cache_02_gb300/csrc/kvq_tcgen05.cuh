@@ -33,15 +33,23 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Bounded wait (about a second); gives up early once ``*abort`` is set by
-// another part of the CTA that will not complete the phase.
-constexpr uint32_t kBarTries = 1u << 22;
+// Bounded wait (a second on the global timer: a try may itself be suspended for
+// long, so a count of tries bounds nothing); gives up early once ``*abort`` is
+// set by another part of the CTA that will not complete the phase.
+constexpr uint64_t kBarNanoseconds = 1000000000;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  for (uint32_t it = 0; it < kBarTries; ++it) {
+  if (bar_try(bar, parity)) return true;
+  uint64_t begun = 0;
+  for (uint32_t it = 1;; ++it) {
     if (bar_try(bar, parity)) return true;
-    if (*abort) return false;
+    if (abort && *abort) return false;
+    if ((it & 63) == 0) {
+      uint64_t now;
+      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+      if (begun == 0) begun = now;
+      if (now - begun > kBarNanoseconds) return false;
+    }
   }
-  return false;
 }
 // A wait that every lane of the warp leaves with the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
@@ -54,10 +62,7 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) bar_arrive(bar);
 }
 // A wait that is not cut short: for copies and MMAs in flight when a CTA stops.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
-  for (uint32_t it = 0; it < kBarTries; ++it)
-    if (bar_try(bar, parity)) return;
-}
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) { bar_wait(bar, parity, nullptr); }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One lane of a converged warp.  A role whose loops and waits are run by the

@@ -10,11 +10,8 @@
 //
 // so a thread owns one key and its sum never leaves a register.  A CTA takes
 // pairs of key tiles: warps 0-3 sum the first, warps 4-7 the second, and both
-// use every query tile that arrives.  Those threads also put the Keys into tensor
-// memory, one row each: with K and Q both read from shared memory the MMAs
-// took all of its bandwidth and every barrier waited for it (80 us for 4096 whole
-// tokens, 32/8 heads of 128, against NEWTIME).  Three score buffers, which
-// the two tiles take in turn, let MMAs and exponentials overlap.  With few
+// use every query tile that arrives.  Each key tile has its own MMA warp and
+// two score buffers, so MMAs, exponentials and the waits overlap.  With few
 // counted queries (at most two tiles) the query tiles stay in shared memory
 // and a run of pairs streams past them; else a CTA has one pair, which stays
 // while the queries stream.  ``split`` CTAs of a cluster take a pair's query
@@ -39,9 +36,9 @@ namespace kvq {
 namespace {
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kWThreads = 384;  // warps 10 and 11 only fill the third warpgroup
+constexpr int kMmaWarp = 8, kCopyWarp = 10, kWThreads = 384;  // MMA warps 8 and 9; 11 only fills the warpgroup
 constexpr int kSumRegs = 200, kOtherRegs = 104;              // a thread, out of the launch's 3 x 168
-constexpr int kQStages = 4, kStayTiles = 2, kSBuffers = 3;
+constexpr int kQStages = 4, kStayTiles = 2;
 
 template <int D>
 struct WLayout {
@@ -54,10 +51,8 @@ struct WLayout {
   static constexpr uint32_t kL = kStay + 2 * kTile, kOnes = kL + kQStages * 2048, kZero = kOnes + 2048;
   static constexpr uint32_t kRed = kZero + 2048;                 // [8 ranks][256 keys]
   static constexpr uint32_t kBars = kRed + 8 * 256 * 4;
-  // K full / empty (2 each), K in tensor memory, Q full / empty, S full / empty
-  static constexpr int kNBars = 5 + 2 * kQStages + 2 * kSBuffers;
-  // tensor memory: key tile w at 64 w, score buffer b at 128 + 128 b
-  static constexpr uint32_t kColS = 128;
+  // K full / empty (2 each), Q full / empty, S full / empty (tile, buffer)
+  static constexpr int kNBars = 4 + 2 * kQStages + 8;
   static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;
 };
 
@@ -73,8 +68,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint8_t* smem = w_raw + ((1024u - (smem_u32(w_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t bar_kf = sbase + L::kBars, bar_ke = bar_kf + 16, bar_kt = bar_ke + 16, bar_qf = bar_kt + 8,
-                 bar_qe = bar_qf + 8 * kQStages, bar_sf = bar_qe + 8 * kQStages, bar_se = bar_sf + 8 * kSBuffers;
+  const uint32_t bar_kf = sbase + L::kBars, bar_ke = bar_kf + 16, bar_qf = bar_ke + 16,
+                 bar_qe = bar_qf + 8 * kQStages, bar_sf = bar_qe + 8 * kQStages, bar_se = bar_sf + 32;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
 
@@ -120,16 +115,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
     *abort = 0;
     for (int i = 0; i < 2; ++i) {
       bar_init(bar_kf + 8 * i, 1);
-      bar_init(bar_ke + 8 * i, 8);  // a warp arrives once, by one lane
+      bar_init(bar_ke + 8 * i, 2);  // both MMA warps
     }
-    bar_init(bar_kt, 8);
     for (int i = 0; i < kQStages; ++i) {
       bar_init(bar_qf + 8 * i, 2);  // the copy, and the warp that wrote -L
-      bar_init(bar_qe + 8 * i, 1);
+      bar_init(bar_qe + 8 * i, 2);  // both MMA warps
     }
-    for (int i = 0; i < kSBuffers; ++i) {
+    for (int i = 0; i < 4; ++i) {
       bar_init(bar_sf + 8 * i, 1);
-      bar_init(bar_se + 8 * i, 4);
+      bar_init(bar_se + 8 * i, 4);  // a warp arrives once, by one lane
     }
     bar_init_fence();
     pdl_wait();
@@ -145,8 +139,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   __syncthreads();
   tm_fence_after();
   const uint32_t tm = *tslot;
-  if (p.split > 1)  // a rank's shared memory is written to only once it runs
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (p.split > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_release();
 
@@ -154,17 +147,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
       // ============ copies; the lanes turn lse into -L =================================
-      auto row_lse = [&](int i, int r) -> float {
-        const int tt = r / p.g, pos = tok0 + i * tile_tok + tt;
-        return tt < tile_tok && pos < sq.len
-                   ? p.lse[(int64_t)(h * p.g + r - tt * p.g) * p.n_tokens + sq.start + pos]
-                   : 0.f;
-      };
+      // the lane's four rows of a tile: their first tile's lse and how many tokens come before the sequence's end
+      // (worked out once: this warp shares its scheduler with two of the summing warps)
+      const float* src[4];
+      int room[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 32 * e + lane, tt = r / p.g;
+        src[e] = p.lse + (int64_t)(h * p.g + r - tt * p.g) * p.n_tokens + sq.start + tok0 + tt;
+        room[e] = tt < tile_tok ? sq.len - tok0 - tt : 0;
+      }
       float ahead[4];
       int ahead_tile = -1;
       auto fetch_lse = [&](int i) {
+        const int at = i * tile_tok;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ahead[e] = row_lse(i, 32 * e + lane);
+        for (int e = 0; e < 4; ++e) ahead[e] = at < room[e] ? src[e][at] : 0.f;
         ahead_tile = i;
       };
       int issued = 0;
@@ -213,45 +211,47 @@ __global__ void __launch_bounds__(kWThreads, 1)
       for (int x = max(0, kpairs - 2); x < kpairs; ++x) bar_drain(bar_kf + 8 * (x & 1), (uint32_t)(x / 2) & 1u);
       for (int x = max(0, issued - kQStages); x < issued; ++x)
         bar_drain(bar_qf + 8 * (x % kQStages), (uint32_t)(x / kQStages) & 1u);
-    } else if (warp == kMmaWarp) {
-      // ============ MMAs, all issued by one lane ========================================
+    } else if (warp < kCopyWarp) {
+      // ============ MMAs of key tile w, issued by one lane ==============================
+      // a warp a tile: one waits while the other issues
       const bool one = elect_one();
       constexpr uint32_t idesc = bf16_idesc(kKeys, kRows, false);
+      const int w = warp - kMmaWarp;
       int taken = 0, n_s = 0;
       bool ok = true;
       for (int pr = 0; pr < pairs && ok; ++pr) {
-        const int both = run0 + pr * 2 * kKeys + kKeys < sq.len;
-        ok = bar_wait(bar_kt, (uint32_t)pr & 1u, abort);
+        const bool active = run0 + (2 * pr + w) * kKeys < sq.len;
+        ok = bar_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort);
         for (int i = q_first(pr); i < nq && ok; i += p.split) {
-          const int s = resident ? i : taken % kQStages;
+          const int s = resident ? i : taken % kQStages, b = 2 * w + (n_s & 1);
           ok = bar_wait(bar_qf + 8 * s, resident ? 0u : (uint32_t)(taken / kQStages) & 1u, abort);
           ++taken;
-          const uint64_t db = sw128_desc(sbase + q_tile(s), 0);
-          for (int w = 0; w < 1 + both && ok; ++w) {
-            const int b = n_s % kSBuffers;
-            if (n_s >= kSBuffers) ok = bar_wait(bar_se + 8 * b, (uint32_t)(n_s / kSBuffers - 1) & 1u, abort);
-            if (!ok) break;
+          if (ok && active) {
+            if (n_s > 1 && !(ok = bar_wait(bar_se + 8 * b, (uint32_t)(n_s / 2 - 1) & 1u, abort))) break;
             tm_fence_after();
-            const uint32_t d = tm + L::kColS + 128 * b;
+            const uint64_t da = sw128_desc(sbase + k_tile(pr, w), 0), db = sw128_desc(sbase + q_tile(s), 0);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              if (one) mma_ts(d, tm + 64 * w + 8 * ks, db + (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2, idesc, ks > 0);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
+              if (one) mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > 0);
+            }
             if (one) {
-              mma_ss(d, plain_desc(sbase + L::kOnes, 2048),
+              mma_ss(tm + 128 * b, plain_desc(sbase + L::kOnes, 2048),
                      plain_desc(sbase + L::kL + s * 2048, L::kZero - L::kL - s * 2048), idesc, 1);
               mma_commit(bar_sf + 8 * b);
             }
             ++n_s;
           }
-          if (one && !resident) mma_commit(bar_qe + 8 * s);
+          if (ok && one && !resident) mma_commit(bar_qe + 8 * s);
         }
+        if (one) mma_commit(bar_ke + 8 * (pr & 1));
       }
       if (!ok) {
         *abort = 1;
         if (one && p.status) atomicOr(p.status, kStatusPromptTimeout);
       }
-      // nothing in flight when the CTA ends: the last commit covers the MMAs before it
-      if (n_s > 0) bar_drain(bar_sf + 8 * ((n_s - 1) % kSBuffers), (uint32_t)((n_s - 1) / kSBuffers) & 1u);
+      // nothing in flight when the CTA ends
+      for (int x = max(0, n_s - 2); x < n_s; ++x) bar_drain(bar_sf + 8 * (2 * w + (x & 1)), (uint32_t)(x / 2) & 1u);
     }
   } else {
     // ============ sums: key tile w, one key a thread ==================================
@@ -259,43 +259,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int w = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float2 sc = make_float2(p.scale2, p.scale2);
-    int n_s = 0;  // score tiles of the CTA before this pair's
+    int n_s = 0;
     bool ok = true;
     for (int pr = 0; pr < pairs && ok; ++pr) {
       const int tile_key = run0 + pr * 2 * kKeys + w * kKeys, key = tile_key + (t & 127);
       const bool active = tile_key < sq.len;
-      const int tiles = run0 + pr * 2 * kKeys + kKeys < sq.len ? 2 : 1;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      // this key's row into tensor memory (the last pair's MMAs are done: their scores were)
-      if (!(ok = warp_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort))) break;
-      if (active) {
-        const uint8_t* row = smem + k_tile(pr, w) + (t & 127) * 128;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {  // 32 channels: four 16-byte pieces, swizzled by row
-          uint32_t x[16];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(x + 4 * e) = *reinterpret_cast<const uint4*>(
-                row + (c / 2) * L::kChunk + (((c & 1) * 4 + e) ^ (t & 7)) * 16);
-          tm_st16(tm + 64 * w + 16 * c + lanes, x);
-        }
-        tm_wait_st();
-        tm_fence_before();
-      }
-      warp_arrive(bar_ke + 8 * (pr & 1));
-      warp_arrive(bar_kt);
-      int n = n_s + w;
-      for (int i = q_first(pr); i < nq; i += p.split, n += tiles) {
-        n_s += tiles;
-        if (!active) continue;
-        const int b = n % kSBuffers;
-        if (!(ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n / kSBuffers) & 1u, abort))) break;
+      for (int i = q_first(pr); i < nq && active; i += p.split) {
+        const int b = 2 * w + (n_s & 1);
+        if (!(ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n_s / 2) & 1u, abort))) break;
+        ++n_s;
         tm_fence_after();
         // rows [lo, hi) of the tile count for this key
         const int pos0 = tok0 + i * tile_tok;
         const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
-        const uint32_t ts = tm + L::kColS + 128 * b + lanes;
+        const uint32_t ts = tm + 128 * b + lanes;
         auto add_tile = [&](auto with_mask) {
           float x[2][32];
           tm_ld32(ts, x[0]);
@@ -326,7 +305,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       sum[0] = add2(sum[0], sum[1]);
       const float mine = sum[0].x + sum[0].y;
       if (p.split > 1) {
-        // into rank 0's shared memory (one pair a CTA)
+        // into rank 0's shared memory (one pair a CTA; every rank runs: it arrived)
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         uint32_t dst = sbase + L::kRed + (uint32_t)(rank * 256 + t) * 4, remote;
         asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(dst));
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(mine) : "memory");
@@ -337,8 +317,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (!ok) {
       *abort = 1;
       if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
+      if (p.split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
   }
+  __syncwarp();
+  if (p.split > 1 && warp >= kMmaWarp) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
@@ -363,20 +346,7 @@ cudaError_t launch_w(const PromptParams& p, const WMaps& maps, int64_t tiles, cu
   const cudaError_t e =
       cudaFuncSetAttribute(weights_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.split));
-  cfg.blockDim = dim3(kWThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.split;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, weights_tc_kernel<D>, p, maps);
+  return launch_cluster(weights_tc_kernel<D>, tiles, p.split, kWThreads, smem, s, p, maps);
 }
 
 }  // namespace
@@ -387,7 +357,7 @@ void weights_tc_plan(int64_t pairs, int64_t most_tokens, int g, int n_sm, int* c
   if (tiles <= kStayTiles) {
     *chunk = (int)std::min<int64_t>(1024, std::max<int64_t>(1, (pairs + n_sm - 1) / n_sm));
   } else {
-    while (*split < 8 && pairs * *split < 2 * n_sm && tiles >= 8 * *split) *split *= 2;
+    while (*split < 8 && pairs * *split < n_sm && tiles >= 8 * *split) *split *= 2;
   }
 }
 
