@@ -12,14 +12,16 @@
 //               attn_full in section 04's appendix, softmax(QK^T / sqrt(d) + M) V)
 //   weights:    w_j = sum over the last queries i >= j of 2^(s_ij - lse_i)
 //
-// Bound: the FMA pipe.  Products run as packed pairs (two channels of a score,
-// two columns of the output): the pipe's rate is the same, but half the issue
-// slots stay free for the shared loads (per four channels 12 wavefronts and 40
-// instructions a warp against 64 cycles of FMA).  Few tiles are split along
-// the keys over a cluster (``split`` CTAs take the key steps in turn) and joined
-// through distributed shared memory in rank order; a causal prompt's last tiles
-// are otherwise what everything waits for.  1999 fp32 tokens, 8/2 heads of 128:
-// NEWFP32 us, 286 us without either.
+// Bound: shared loads and the FMA pipe together.  Per four channels a warp takes
+// 24 wavefronts (a 16-byte load of 32 rows is 4, of two broadcast rows 2) and, as
+// packed pairs (two channels of a score, two columns of the output; half the
+// issue slots of single products), 32 cycles of FMA for each of the SM's four
+// schedulers.  Few tiles are split along the keys over a cluster (``split`` CTAs
+// take the key steps in turn) and joined through distributed shared memory in rank
+// order; a causal prompt's last tiles are otherwise what everything waits for.
+// 1999 fp32 tokens, 8/2 heads of 128: 252 us, 286 us without either.  Tiles of 128
+// x 128 with 8 x 8 a thread halve the loads but leave two warps a scheduler
+// to hide them (285 us); a second buffer for V changes nothing.
 
 #include <cuda_bf16.h>
 
