@@ -7,12 +7,15 @@
 // keys in blocks of 128, both tiles on the same Key and Value tile:
 //
 //   S_i = Q_i K^T       128 x 128, fp32 in tensor memory (Q, K from shared memory)
-//   P_i = 2^(S_i c - m) bf16, over S_i in tensor memory
+//   P_i = 2^(S_i c - m) bf16, in tensor memory
 //   O_i += P_i V        128 x d, fp32 in tensor memory (P from tensor memory)
 //
 // Warps 0-3 and 4-7 run the softmax of tile 0 and 1, one row a thread, so
 // maxima and sums need no exchange; warp 8 issues the MMAs, warp 9 the TMA
-// copies.  The tiles alternate: one tile's MMAs run under the other's softmax.
+// copies.  At d = 128 tensor memory holds S, with P over it, and O: the tiles
+// alternate, one's MMAs run under the other's softmax.  At d = 64 P has columns
+// of its own, S_i is free once its rows are in registers, and the next block's
+// Q K^T runs under the same tile's softmax too (NEWD64).
 // The running maximum moves only when a score passes it by 2^8 (a row's sums
 // stay exact in fp32 either way), so O is rescaled rarely and by the softmax
 // threads themselves.
@@ -37,10 +40,12 @@ struct TcLayout {
   static constexpr uint32_t kChunk = 128 * 128;           // 128 rows of 64 channels
   static constexpr uint32_t kTile = kChunk * (D / 64);    // a Q, K or V tile
   static constexpr uint32_t kQ = 0, kK0 = 2 * kTile, kRing = 3 * kTile, kBars = kRing + 2 * kSlots * kTile;
-  // barriers: full and empty per slot, K_0, the cleared Value rows, then per tile: Q, S, P (two halves), O
-  static constexpr int kNBars = 2 * kSlots + 2 + 10;
+  // barriers: full and empty per slot, K_0, the cleared Value rows, then per tile: Q, S, P (two halves), O, S read
+  static constexpr int kNBars = 2 * kSlots + 2 + 12;
+  static constexpr bool kApart = D == 64;                 // P beside S, not over it
   static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;  // + alignment
-  static constexpr uint32_t kColS = 0, kColO = 256;       // S_i at 128 i, O_i at 256 + D i
+  // S_i at 128 i, O_i at 256 + D i, P_i over S_i or at 384 + 64 i
+  static constexpr uint32_t kColS = 0, kColO = 256, kColP = kApart ? 384 : 0, kStepP = kApart ? 64 : 128;
 };
 
 struct TcMaps {
@@ -57,7 +62,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kSlots;
   const uint32_t bar_k0 = bar_empty + 8 * L::kSlots, bar_clear = bar_k0 + 8, bar_q = bar_clear + 8, bar_s = bar_q + 16,
-                 bar_p = bar_s + 16, bar_o = bar_p + 32;
+                 bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
 
@@ -111,6 +116,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bar_init(bar_p + 16 * i, 4);  // a warp arrives once, by one lane
       bar_init(bar_p + 16 * i + 8, 4);
       bar_init(bar_o + 8 * i, 1);
+      bar_init(bar_r + 8 * i, 4);
     }
     bar_init_fence();
     pdl_wait();
@@ -161,9 +167,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (n1 > 0) bar_drain(bar_q + 8, 0);
     } else if (warp == kMmaWarp) {
       // ============ MMAs, all issued by one lane ======================================
-      // The MMAs run in the order of issue, so Q K^T of the next block may
-      // overwrite P (it shares S's columns) right behind the P V that reads it,
-      // and the arrival for S_j also says that the P V of block j - 1 is done.
+      // The MMAs run in the order of issue.  With P over S, Q K^T of the next
+      // block may therefore overwrite P right behind the P V that reads it, and
+      // the arrival for S_j also says that the P V of block j - 1 is done.  With P
+      // apart, O's barrier says so, once a block.
       constexpr uint32_t idesc_s = bf16_idesc(kRows, kKeys, false), idesc_o = bf16_idesc(kRows, D, true);
       const bool one = elect_one();
       auto scores = [&](int i, uint32_t kaddr) {
@@ -189,13 +196,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int s = j % L::kSlots;
         const uint32_t vaddr = sbase + L::kRing + 2 * s * L::kTile, kaddr = vaddr + L::kTile;
         if (clear && j == nmax - 1) ok = bar_wait(bar_clear, 0, abort);
+        if (L::kApart) {
+          for (int i = 0; i < 2 && ok; ++i) {
+            if (j + 1 >= (i ? n1 : n0)) continue;
+            if (!(ok = bar_wait(bar_r + 8 * i, (uint32_t)j & 1u, abort))) break;
+            tm_fence_after();
+            scores(i, kaddr);
+          }
+        }
         for (int i = 0; i < 2 && ok; ++i) {
           const int ni = i ? n1 : n0;
           if (j >= ni) continue;
           const uint64_t b = sw128_desc(vaddr, L::kChunk);
           const int steps = min(8, ((i ? end1 : end0) - j * kKeys + 15) / 16);
           auto values = [&](int ks) {
-            if (one) mma_ts(tm + L::kColO + D * i, tm + L::kColS + 128 * i + 8 * ks, b + ks * (2048 >> 4), idesc_o,
+            if (one) mma_ts(tm + L::kColO + D * i, tm + L::kColP + L::kStepP * i + 8 * ks, b + ks * (2048 >> 4), idesc_o,
                             j > 0 || ks > 0);
           };
           if (!(ok = bar_wait(bar_p + 16 * i, (uint32_t)j & 1u, abort))) break;
@@ -208,22 +223,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int ks = 4; ks < 8; ++ks)
             if (ks < steps) values(ks);
+          if (one && (L::kApart || j + 1 == ni)) mma_commit(bar_o + 8 * i);
           // the next pair's wait passes while MMAs are queued
           if (i == (n1 > 0) && j + 1 < nmax) ok = landed(j + 1);
-          if (j + 1 < ni) scores(i, kaddr);
-          else if (one) mma_commit(bar_o + 8 * i);
+          if (!L::kApart && j + 1 < ni) scores(i, kaddr);
         }
         if (ok && one) mma_commit(bar_empty + 8 * s);
       }
       if (!ok) {
-        // stopped early: nothing in flight when the CTA ends (bar_o's first phase may be over)
+        // stopped early: nothing in flight when the CTA ends (bar_k0's one phase is over, unless K_0 never came)
         *abort = 1;
         if (one) {
           if (p.status) atomicOr(p.status, kStatusPromptTimeout);
-          mma_commit(bar_o);
-          bar_drain(bar_o, 0);
-          mma_commit(bar_o);
-          bar_drain(bar_o, 1);
+          mma_commit(bar_k0);
+          bar_drain(bar_k0, 1);
         }
       }
     }
@@ -236,7 +249,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const bool live = tt < tile_tok && pos < sq.len;
     const bool warp_live = __any_sync(0xffffffffu, live);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tm + L::kColS + 128 * i + lanes, to = tm + L::kColO + D * i + lanes;
+    const uint32_t ts = tm + L::kColS + 128 * i + lanes, to = tm + L::kColO + D * i + lanes,
+                   tp = tm + L::kColP + L::kStepP * i + lanes;
     const float2 sc = make_float2(p.scale2, p.scale2);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -248,6 +262,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tm_ld32(ts + 32 * c, s + 32 * c);
         tm_wait_ld();
+        if (L::kApart) {
+          tm_fence_before();
+          warp_arrive(bar_r + 8 * i);
+        }
         const int limit = pos - j * kKeys;  // the last key of the block this row sees
         if (__any_sync(0xffffffffu, limit < kKeys - 1)) {
 #pragma unroll
@@ -263,6 +281,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
         const bool up = top > m + kSlack;
+        if (L::kApart && j > 0) {  // the last block's P V is done with P and with O
+          if (!(ok = warp_wait(bar_o + 8 * i, (uint32_t)(j - 1) & 1u, abort))) break;
+          tm_fence_after();
+        }
         if (__any_sync(0xffffffffu, up)) {
           const float a = up ? ex2(m - top) : 1.f;
           if (up) m = top;
@@ -292,7 +314,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
             w[e / 2] = pack_bf16(x.x, x.y);
           }
-          tm_st16(ts + c / 2, w);
+          tm_st16(tp + c / 2, w);
           if (c == 32) {  // the first 64 keys' weights: their P V may start
             tm_wait_st();
             tm_fence_before();
@@ -304,11 +326,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_wait_st();
         tm_fence_before();
       } else {
+        if (L::kApart) {
+          // like the others, so that no arrival counts for the block before
+          warp_arrive(bar_r + 8 * i);
+          if (j > 0 && !(ok = warp_wait(bar_o + 8 * i, (uint32_t)(j - 1) & 1u, abort))) break;
+        }
         warp_arrive(bar_p + 16 * i);
       }
       warp_arrive(bar_p + 16 * i + 8);
     }
-    if (ok && n > 0) ok = warp_wait(bar_o + 8 * i, 0, abort);
+    if (ok && n > 0) ok = warp_wait(bar_o + 8 * i, L::kApart ? (uint32_t)(n - 1) & 1u : 0u, abort);
     if (!ok) {
       *abort = 1;
       if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
