@@ -302,29 +302,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         const float2 nm = make_float2(-m, -m);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t w[16];
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
+          for (int e = 0; e < 64; e += 2) {
             float2 x = fma2(make_float2(s[c + e], s[c + e + 1]), sc, nm);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
-            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
+            sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], x);
             w[e / 2] = pack_bf16(x.x, x.y);
           }
-          tm_st16(tp + c / 2, w);
-          if (c == 32) {  // the first 64 keys' weights: their P V may start
-            tm_wait_st();
-            tm_fence_before();
-            warp_arrive(bar_p + 16 * i);
-          }
+          tm_st32(tp + c / 2, reinterpret_cast<const float*>(w));
+          tm_wait_st();
+          tm_fence_before();
+          if (c == 0) warp_arrive(bar_p + 16 * i);  // the first 64 keys' weights: their P V may start
         }
-        sum[0] = add2(sum[0], sum[1]);
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
-        tm_wait_st();
-        tm_fence_before();
       } else {
         if (L::kApart) {
           // like the others, so that no arrival counts for the block before
