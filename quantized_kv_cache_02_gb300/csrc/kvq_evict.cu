@@ -13,9 +13,10 @@
 // CTAs an SM) 56 and 41 us, and passes of 11 bits, whose 2048 counters are read from
 // every peer, 163 us.
 //
-// Gather.  A thread has four 16-byte pieces of K and of V in flight.  Bound by
-// HBM: 16 bytes a kept piece read and written.  Small choices gather in the
-// choosing CTA and save the second launch.
+// Gather.  The unit's CTAs then copy its rows, an equal share each, with four
+// 16-byte pieces of K and of V in flight a thread.  Bound by HBM: 16 bytes a kept
+// piece read and written.  (A second kernel for the copies has every SM for few
+// units but starts 3 us later and costs the host a launch: EVGATHER.)
 
 #include <algorithm>
 #include <atomic>
@@ -28,7 +29,6 @@ namespace {
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kCached = 55 * 1024;   // words of a run that shared memory holds; a longer one is read again a pass
-constexpr int kGatherThreads = 256, kPieces = 4 * kGatherThreads;
 
 // Weights in increasing order as unsigned words: -0 equals 0, NaN is lowest.
 __device__ __forceinline__ uint32_t order_bits(float w) {
@@ -79,38 +79,41 @@ __device__ __forceinline__ uint4 peer_words(const uint32_t* p, int rank) {
   return v;
 }
 
-// Copy kept rows [r0, r0 + rows) of a unit.
-__device__ __forceinline__ void gather_rows(const EvictParams& p, const EvictSeq& sq, int h, int64_t r0, int rows,
-                                            int per, int t, int threads) {
-  const int64_t base = sq.out_row + (int64_t)h * sq.keep + r0;
-  const int n = rows * per;
-  for (int i0 = t; i0 < n; i0 += 4 * threads) {
-    uint4 a[4], b[4];
+// Copy kept rows [r0, r1) of a unit.
+__device__ __forceinline__ void gather_rows(const EvictParams& p, const EvictSeq& sq, int h, int r0, int r1, int t) {
+  constexpr int kBlock = 1 << 16;  // rows whose pieces an int counts
+  const int per = p.row_bytes / 16;
+  for (int64_t rb = r0; rb < r1; rb += kBlock) {
+    const int64_t base = sq.out_row + (int64_t)h * sq.keep + rb;
+    const int n = (int)min((int64_t)kBlock, r1 - rb) * per;
+    for (int i0 = t; i0 < n; i0 += 4 * kSelThreads) {
+      uint4 a[4], b[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e * threads;
-      if (i < n) {
-        const int r = i / per, c = (i - r * per) * 16;
-        const int64_t tok = (int64_t)sq.start + p.index[base + r];
-        a[e] = __ldcs(reinterpret_cast<const uint4*>(p.k + tok * p.k_ts + (int64_t)h * p.k_hs + c));
-        b[e] = __ldcs(reinterpret_cast<const uint4*>(p.v + tok * p.v_ts + (int64_t)h * p.v_hs + c));
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kSelThreads;
+        if (i < n) {
+          const int r = i / per, c = (i - r * per) * 16;
+          const int64_t tok = (int64_t)sq.start + p.index[base + r];
+          a[e] = __ldcs(reinterpret_cast<const uint4*>(p.k + tok * p.k_ts + (int64_t)h * p.k_hs + c));
+          b[e] = __ldcs(reinterpret_cast<const uint4*>(p.v + tok * p.v_ts + (int64_t)h * p.v_hs + c));
+        }
       }
-    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e * threads;
-      if (i < n) {
-        const int r = i / per, c = (i - r * per) * 16;
-        *reinterpret_cast<uint4*>(p.k_out + (base + r) * p.row_bytes + c) = a[e];
-        *reinterpret_cast<uint4*>(p.v_out + (base + r) * p.row_bytes + c) = b[e];
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kSelThreads;
+        if (i < n) {
+          const int r = i / per, c = (i - r * per) * 16;
+          *reinterpret_cast<uint4*>(p.k_out + (base + r) * p.row_bytes + c) = a[e];
+          *reinterpret_cast<uint4*>(p.v_out + (base + r) * p.row_bytes + c) = b[e];
+        }
       }
     }
   }
 }
 
-// CLUSTER: a cluster a unit; else one CTA, which may also copy the rows.
+// CLUSTER: a cluster a unit; else one CTA.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads) evict_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint8_t sel_smem[];
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_smem);
   uint32_t* run = reinterpret_cast<uint32_t*>(sel_smem + sizeof(SelShared));
@@ -262,23 +265,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
           n_equal += x == prefix;
         }
       }
-      if (CLUSTER) unit_barrier<CLUSTER>();  // no rank ends while another reads its counts
     }
   }
-  if (!CLUSTER && p.gather_here) {
-    __syncthreads();
-    gather_rows(p, sq, h, 0, sq.keep, p.row_bytes / 16, t, kSelThreads);
-  }
-}
-
-__global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __grid_constant__ EvictParams p) {
-  const EvictSeq sq = p.seq[blockIdx.z];
-  const int per = p.row_bytes / 16, rows = kPieces / per;
-  const int64_t r0 = (int64_t)blockIdx.x * rows;
-  pdl_wait();
-  pdl_release();
-  if (r0 < sq.keep)
-    gather_rows(p, sq, blockIdx.y, r0, (int)min((int64_t)rows, sq.keep - r0), per, threadIdx.x, kGatherThreads);
+  unit_barrier<CLUSTER>();  // the indices are written, and no rank reads another's counts any more
+  gather_rows(p, sq, h, (int)((int64_t)sq.keep * rank / size), (int)((int64_t)sq.keep * (rank + 1) / size), t);
 }
 
 }  // namespace
@@ -301,7 +291,7 @@ static int active_clusters(int size) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<true>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, evict_kernel<true>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -309,24 +299,22 @@ static int active_clusters(int size) {
   return n;
 }
 
-cudaError_t launch_evict(EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s, int* launches) {
-  // the largest cluster that leaves each CTA 4096 tokens and lets every unit run
-  // at once; more units than that fill the GPU with one CTA each
+cudaError_t launch_evict(const EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s) {
+  // the largest cluster that lets every unit run at once and still leaves each
+  // CTA 8192 tokens to choose from or 64 KB of rows to copy; more units than that
+  // fill the GPU with one CTA each
   int size = 1;
-  const int64_t units = (int64_t)p.Hkv * p.n_seqs;
-  if (max_len >= 8192) {
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const int64_t units = (int64_t)p.Hkv * p.n_seqs, bytes = 2 * (int64_t)max_keep * p.row_bytes;
+  if (max_len >= 2 * 8192 || bytes >= 2 * 65536) {
+    cudaError_t e = cudaFuncSetAttribute(evict_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     for (int c : {2, 4, 8, 12, 16})
-      if ((int64_t)c * 4096 <= max_len && units <= active_clusters(c)) size = c;
+      if ((max_len >= c * 8192 || bytes >= c * 65536) && units <= active_clusters(c)) size = c;
   }
   const int share = (max_len + size - 1) / size;
   const size_t smem = sizeof(SelShared) + (size_t)std::min(share, kCached) * sizeof(uint32_t);
-  // up to 64 KB of rows a unit the choosing CTA copies them itself
-  p.gather_here = size == 1 && (int64_t)max_keep * p.row_bytes <= 32 * 1024;
-  const auto kernel = size > 1 ? evict_select_kernel<true> : evict_select_kernel<false>;
+  const auto kernel = size > 1 ? evict_kernel<true> : evict_kernel<false>;
   cudaError_t e = cudaSuccess;
   if (size == 1) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax);
   if (e != cudaSuccess) return e;
@@ -343,13 +331,7 @@ cudaError_t launch_evict(EvictParams& p, int32_t max_len, int32_t max_keep, cuda
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = size > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
-  *launches = 1;
-  if (e != cudaSuccess || p.gather_here) return e;
-  const int rows = kPieces / (p.row_bytes / 16);
-  *launches = 2;
-  return launch_pdl(evict_gather_kernel, dim3((unsigned)((max_keep + rows - 1) / rows), p.Hkv, p.n_seqs),
-                    dim3(kGatherThreads), 0, s, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace kvq

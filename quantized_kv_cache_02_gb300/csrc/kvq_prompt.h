@@ -72,7 +72,6 @@ struct EvictSeq {
 struct EvictParams {
   int32_t Hkv, row_bytes;      // bytes of one token's head
   int32_t first, recent;
-  int32_t gather_here;         // the choosing CTA also copies the rows (set by launch_evict)
   const uint8_t* k;
   const uint8_t* v;
   int64_t k_ts, k_hs, v_ts, v_hs;  // bytes
@@ -110,7 +109,7 @@ cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, 
 // CTAs that share a tile of the CUDA-core attention
 int prompt_simt_split(int64_t tiles, int32_t max_len, int n_sm);
 cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
-cudaError_t launch_evict(EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s, int* launches);
+cudaError_t launch_evict(const EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s);
 
 // the tensor-core attention (bf16, head_dim 64 or 128); a tile of its order is
 // prompt_tc_tokens(g) tokens

@@ -352,10 +352,9 @@ kvq_status evict(const kvq_prompt* p, const void* k, const void* v, const float*
       row += keep[i] * p->n_kv_heads;
     }
     if (ep.n_seqs == 0) continue;
-    int n = 0;
-    const cudaError_t e = kvq::launch_evict(ep, max_len, max_keep, static_cast<cudaStream_t>(stream), &n);
+    const cudaError_t e = kvq::launch_evict(ep, max_len, max_keep, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "evict launch");
-    kvq::count_launches((uint64_t)n);
+    kvq::count_launches(1);
   }
   return KVQ_OK;
 }
