@@ -447,8 +447,10 @@ kvq_status kvq_compare(const void* key, const void* value, int64_t batch, int32_
  * NULL).  Scores, softmax statistics and the output sum are fp32; for bf16 the
  * softmax weights are rounded to bf16 before they meet v.  One sequence's
  * values never reach another's result, whatever they hold; inside a sequence
- * finite values are assumed (as everywhere in this library).  out must not
- * overlap the inputs.  Only enqueues work on ``stream``; needs no workspace, and
+ * finite values are assumed (as everywhere in this library), Values small enough
+ * for fp32 sums of 2^8 times their size.  out must not overlap the inputs, nor
+ * its rows each other.  No gradient: like the rest of the library this serves
+ * inference.  Only enqueues work on ``stream``; needs no workspace, and
  * two calls may run at once.  Errors before any launch: KVQ_EINVAL (shape,
  * stride, length, NULL or misaligned pointer, or memory that is not on the
  * current device), KVQ_EUNSUPPORTED (head_dim, g, strides of 2^40 bytes). */

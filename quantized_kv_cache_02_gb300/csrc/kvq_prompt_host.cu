@@ -88,8 +88,19 @@ kvq_status check_tensor(const kvq_prompt* p, const char* name, const void* ptr, 
   if ((p->n_tokens > 1 && (ts < p->head_dim || ts % step)) || (heads > 1 && (hs < p->head_dim || hs % step)))
     return fail(KVQ_EINVAL, "%s strides (token %lld, head %lld) must be multiples of %lld elements and at least head_dim",
                 name, (long long)ts, (long long)hs, (long long)step);
-  if (std::max(ts, hs) >= (int64_t(1) << 40) / esize_of(p))
+  const int64_t most = (int64_t(1) << 40) / esize_of(p);
+  if ((p->n_tokens > 1 && ts >= most) || (heads > 1 && hs >= most))
     return fail(KVQ_EUNSUPPORTED, "%s strides must be below 2^40 bytes", name);
+  return KVQ_OK;
+}
+
+// No two of out's rows may share memory.
+kvq_status check_out(const kvq_prompt* p, const void* ptr) {
+  const int64_t ts = p->out_token_stride, hs = p->out_head_stride, d = p->head_dim;
+  const kvq_status st = check_tensor(p, "out", ptr, ts, hs, p->n_q_heads);
+  if (st != KVQ_OK) return st;
+  if (p->n_tokens > 1 && p->n_q_heads > 1 && hs * (p->n_q_heads - 1) + d > ts && ts * (p->n_tokens - 1) + d > hs)
+    return fail(KVQ_EINVAL, "out strides (token %lld, head %lld) make its rows overlap", (long long)ts, (long long)hs);
   return KVQ_OK;
 }
 
@@ -212,7 +223,7 @@ kvq_status prompt_attention(const kvq_prompt* p, const void* q, const void* k, c
   KVQ_TRY(check_tensor(p, "q", q, p->q_token_stride, p->q_head_stride, p->n_q_heads));
   KVQ_TRY(check_tensor(p, "k", k, p->k_token_stride, p->k_head_stride, p->n_kv_heads));
   KVQ_TRY(check_tensor(p, "v", v, p->v_token_stride, p->v_head_stride, p->n_kv_heads));
-  KVQ_TRY(check_tensor(p, "out", out, p->out_token_stride, p->out_head_stride, p->n_q_heads));
+  KVQ_TRY(check_out(p, out));
   KVQ_TRY(check_on_device("q", q));
   KVQ_TRY(check_on_device("k", k));
   KVQ_TRY(check_on_device("v", v));
@@ -278,9 +289,11 @@ kvq_status prompt_weights(const kvq_prompt* p, const void* q, const void* k, con
     kvq::weights_tc_plan(pairs, std::min<int64_t>(last, l[0].len), pp.g, n_sm, &chunk, &pp.split);
     return 256 * chunk;
   };
-  for (const auto& l : launches)
-    if (fill_tiles(l, pp.Hkv, step_of(l), &pp.tiles) * pp.split > kMaxTiles)
+  for (const auto& l : launches) {
+    const int step = step_of(l);  // sets pp.split
+    if (fill_tiles(l, pp.Hkv, step, &pp.tiles) > kMaxTiles / pp.split)
       return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
+  }
   for (const auto& l : launches) {
     const int64_t tiles = fill_tiles(l, pp.Hkv, step_of(l), &pp.tiles);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

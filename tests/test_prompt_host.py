@@ -65,6 +65,17 @@ def test_strides(bad, status):
     assert attention(p) == weights(p) == evict(p) == status
 
 
+def test_rows_of_out_do_not_overlap():
+    p, keep_alive = prompt(out_token_stride=64, out_head_stride=64)
+    assert attention(p) == B.KVQ_EINVAL
+    p, keep_alive = prompt(out_token_stride=448, out_head_stride=64)
+    assert attention(p) == B.KVQ_EINVAL
+    assert b"overlap" in kvq.load_library().kvq_last_error()
+    # strides of a dimension of one entry are not looked at
+    p, keep_alive = prompt(lens=(1,), n_tokens=1, k_token_stride=0, k_head_stride=60)
+    assert attention(p) == B.KVQ_EINVAL and b"k strides" in kvq.load_library().kvq_last_error()
+
+
 def test_pointers():
     p, keep_alive = prompt()
     null = ctypes.c_void_p()
