@@ -8,15 +8,17 @@
 // order-preserving words.  A radix select finds the left-th largest word eight
 // bits at a time (each CTA counts its run, all add up every CTA's 256 counts
 // through distributed shared memory: one cluster barrier a pass); one ordered
-// pass then writes the kept tokens.  Every weight is read once.  Eight
-// units of 432,000 tokens take 34 us as clusters of 12 that run at once; of 16 (two waves, or two
-// CTAs an SM) 56 and 41 us, and passes of 11 bits, whose 2048 counters are read from
-// every peer, 163 us.
+// pass then writes the kept tokens.  Every weight is read once.
+// Eight units of 432,000 tokens take 27 us as clusters of 12, which run at
+// once; of 16 (in two waves, or two CTAs an SM) 56 and 41 us, and passes of 11
+// bits, whose 2048 counters are read from every peer, 163 us.
 //
 // Gather.  The unit's CTAs then copy its rows, an equal share each, with four
 // 16-byte pieces of K and of V in flight a thread.  Bound by HBM: 16 bytes a kept
-// piece read and written.  (A second kernel for the copies has every SM for few
-// units but starts 3 us later and costs the host a launch: EVGATHER.)
+// piece read and written.  A second kernel for the copies has every SM for few
+// units but starts later and costs the host a launch: eight ragged prompts (67 MB
+// in all) 22.8 us against 19.6 us, one of 432,000 tokens (132 MB) 47.7 us against
+// 48.5 us.
 
 #include <algorithm>
 #include <atomic>
@@ -159,11 +161,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_kernel(const __grid_constan
         const int shift = 24 - 8 * pass;
         uint32_t* hist = sh.hist[pass];
         if (pass > 0) {
-#pragma unroll 4
-          for (int i = t; i < n; i += kSelThreads) {
-            const uint32_t x = word(i);
+          auto count = [&](uint32_t x) {
             if (x >> (shift + 8) == prefix) atomicAdd(&hist[(x >> shift) & 255u], 1u);
+          };
+          const int fours = cached ? n / 4 : 0;
+#pragma unroll 2
+          for (int i = t; i < fours; i += kSelThreads) {
+            const uint4 x = reinterpret_cast<const uint4*>(run)[i];
+            count(x.x);
+            count(x.y);
+            count(x.z);
+            count(x.w);
           }
+          for (int i = 4 * fours + t; i < n; i += kSelThreads) count(word(i));
         }
         unit_barrier<CLUSTER>();
         const uint32_t* sums = hist;
@@ -213,12 +223,25 @@ __global__ void __launch_bounds__(kSelThreads) evict_kernel(const __grid_constan
       // it.  A thread counts a stretch of the run (of odd length: no two lanes on
       // one bank), then writes its kept tokens from where those before it end.
       const int stretch = (n + kSelThreads - 1) / kSelThreads | 1, s0 = min(n, t * stretch), s1 = min(n, s0 + stretch);
+      // (of at most 64 words it remembers which, and need not look at the others again)
       uint32_t above = 0, equal = 0;
+      uint64_t ups = 0, ties = 0;
+      const bool remember = stretch <= 64;
+      if (remember) {
 #pragma unroll 4
-      for (int i = s0; i < s1; ++i) {
-        const uint32_t x = word(i);
-        above += x > prefix;
-        equal += x == prefix;
+        for (int i = s0; i < s1; ++i) {
+          const uint32_t x = word(i);
+          ups |= (uint64_t)(x > prefix) << (i - s0);
+          ties |= (uint64_t)(x == prefix) << (i - s0);
+        }
+        above = (uint32_t)__popcll(ups);
+        equal = (uint32_t)__popcll(ties);
+      } else {
+        for (int i = s0; i < s1; ++i) {
+          const uint32_t x = word(i);
+          above += x > prefix;
+          equal += x == prefix;
+        }
       }
       uint32_t n_above = above, n_equal = equal;  // running sums over the threads, this one's included
 #pragma unroll
@@ -257,12 +280,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_kernel(const __grid_constan
         n_above += __reduce_add_sync(0xffffffffu, ra);
         n_equal += __reduce_add_sync(0xffffffffu, re);
       }
-      if (above + equal > 0) {
+      auto give = [&](int i, bool up, bool tie) {
+        if (up || (tie && n_equal < need)) out[lo + n_above + min(n_equal, need)] = r0 + i;
+        n_above += up;
+        n_equal += tie;
+      };
+      if (remember) {
+        for (uint64_t left_of = ups | ties; left_of; left_of &= left_of - 1) {
+          const int e = __ffsll((long long)left_of) - 1;
+          give(s0 + e, ups >> e & 1u, ties >> e & 1u);
+        }
+      } else if (above + equal > 0) {
         for (int i = s0; i < s1; ++i) {
           const uint32_t x = word(i);
-          if (x > prefix || (x == prefix && n_equal < need)) out[lo + n_above + min(n_equal, need)] = r0 + i;
-          n_above += x > prefix;
-          n_equal += x == prefix;
+          give(i, x > prefix, x == prefix);
         }
       }
     }

@@ -180,13 +180,19 @@ int64_t fill_tiles(const std::vector<kvq::PromptSeq>& seqs, int hkv, int step, k
 
 // The tensor cores round every accumulation toward zero (Fasi, Higham, Mikaitis
 // and Pranesh, "Numerical behavior of NVIDIA tensor cores", 2021): a score loses
-// half a step of each of its D / 16 partial sums on average, which grow about
-// evenly, and a step is 2^-23 / (2 ln 2) of its number on average.  The relative
-// loss, by which the scores' factor is raised: without it the weights of a
-// 4096-token prompt were 4.5e-6 off, 7.7e-7.
-double rounding_loss(int head_dim) {
-  const double steps = head_dim / 16, sums = (steps + 1) / 2;
-  return 0.5 * sums * std::ldexp(1.0, -23) / (2.0 * std::log(2.0));
+// half a step of each partial sum on average, and a step is 2^-23 / (2 ln 2) of
+// its number on average.  The relative loss of a score whose partial sums add up to
+// ``sums`` times its size, by which its factor is raised.
+double rounding_loss(double sums) { return 0.5 * sums * std::ldexp(1.0, -23) / (2.0 * std::log(2.0)); }
+
+// sqrt(d) for the scores: their factor, and lse in their units -- on the tensor
+// cores before the factor, else after it -- as a factor in two floats.
+void set_scale(const kvq_prompt* p, double loss, kvq::PromptParams* pp) {
+  const double root = std::sqrt((double)p->head_dim);
+  pp->scale2 = (float)(1.4426950408889634 / root * (1.0 + loss));
+  const double r = tensor_cores(p) ? root / (1.0 + loss) : root * (double)pp->scale2;
+  pp->lse_hi = (float)r;
+  pp->lse_lo = (float)(r - (double)pp->lse_hi);
 }
 
 void base_params(const kvq_prompt* p, kvq::PromptParams* pp) {
@@ -195,14 +201,6 @@ void base_params(const kvq_prompt* p, kvq::PromptParams* pp) {
   pp->Hq = p->n_q_heads;
   pp->Hkv = p->n_kv_heads;
   pp->g = p->n_q_heads / p->n_kv_heads;
-  const double loss = tensor_cores(p) ? rounding_loss(p->head_dim) : 0.0;
-  pp->scale2 = (float)(1.4426950408889634 / std::sqrt((double)p->head_dim) * (1.0 + loss));
-  // lse in the units of the scores -- on the tensor cores before scale2, else after it -- is this
-  // factor times lse, as two floats
-  const double r = tensor_cores(p) ? std::sqrt((double)p->head_dim) / (1.0 + loss)
-                                   : std::sqrt((double)p->head_dim) * (double)pp->scale2;
-  pp->lse_hi = (float)r;
-  pp->lse_lo = (float)(r - (double)pp->lse_hi);
   pp->q_ts = p->q_token_stride;
   pp->q_hs = p->q_head_stride;
   pp->k_ts = p->k_token_stride;
@@ -237,6 +235,8 @@ kvq_status prompt_attention(const kvq_prompt* p, const void* q, const void* k, c
   pp.v = v;
   pp.out = out;
   pp.lse = lse;
+  // D / 16 partial sums that grow evenly
+  set_scale(p, tensor_cores(p) ? rounding_loss((p->head_dim / 16 + 1) / 2.0) : 0.0, &pp);
   const bool tc = tensor_cores(p);
   const int step = tc ? kvq::prompt_tc_tokens(pp.g) : kvq::kPromptRows / pp.g;
   int n_sm = 0;
@@ -276,6 +276,11 @@ kvq_status prompt_weights(const kvq_prompt* p, const void* q, const void* k, con
   pp.lse = const_cast<float*>(lse);
   pp.weights = weights;
   pp.last = last;
+  // two halves of D / 32 partial sums that grow to half the score, and, of the
+  // scores that count, the second less lse, which loses half the other way.
+  // Unraised, the weights of a 4096-token prompt were 4.5e-6 off; of whole
+  // scores, raised, 1.1e-6; so, HALFERR.
+  set_scale(p, tensor_cores(p) ? rounding_loss((p->head_dim / 32 + 1) / 2.0 - 0.5) : 0.0, &pp);
   pp.split = 1;
   const bool tc = tensor_cores(p);
   int n_sm = 0;

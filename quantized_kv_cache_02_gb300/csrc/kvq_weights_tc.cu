@@ -10,8 +10,8 @@
 //
 // so a thread owns one key and its sum never leaves a register.  A CTA takes
 // pairs of key tiles: warps 0-3 sum the first, warps 4-7 the second, and both
-// use every query tile that arrives.  Each key tile has its own MMA warp and
-// two score buffers, so MMAs, exponentials and the waits overlap.  With few
+// use every query tile that arrives.  Each key tile has its own MMA warp, so
+// MMAs, exponentials and the waits overlap.  With few
 // counted queries (at most two tiles) the query tiles stay in shared memory
 // and a run of pairs streams past them; else a CTA has one pair, which stays
 // while the queries stream.  ``split`` CTAs of a cluster take a pair's query
@@ -22,8 +22,17 @@
 // score, as four bf16 pieces against a column of ones, so an element costs one
 // multiplication, one exponential and one addition, and no load of its own.
 // (Read per column from shared memory instead, the loads took the bandwidth that
-// the MMAs' operands need: 123 us against NEWTIME for 4096 whole tokens, 32/8
-// heads of 128.)
+// the MMAs' operands need: 123 us, then 80 us, for 4096 whole tokens, 32/8 heads
+// of 128; 64 us with a MMA warp a tile and no more CTAs a pair than fill the SMs.)
+//
+// A score is two sums, over the first and the last half of the channels, added by
+// the thread: the tensor cores round every accumulation toward zero, by more the
+// larger the sum, and four steps of half the size lose less than half of eight.
+// The thread holds the first half in registers, so its buffer fills with the next
+// tile's while this tile's second half is read.
+//
+// Bound: per pair and query tile 9/8 of 1024 cycles of MMA and 1024 of
+// exponentials on each scheduler; measured, about 1500 of both together.
 // ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d) + M).)
 
 #include <algorithm>
@@ -51,7 +60,7 @@ struct WLayout {
   static constexpr uint32_t kL = kStay + 2 * kTile, kOnes = kL + kQStages * 2048, kZero = kOnes + 2048;
   static constexpr uint32_t kRed = kZero + 2048;                 // [8 ranks][256 keys]
   static constexpr uint32_t kBars = kRed + 8 * 256 * 4;
-  // K full / empty (2 each), Q full / empty, S full / empty (tile, buffer)
+  // K full / empty (2 each), Q full / empty, S full / empty (tile, half of the channels)
   static constexpr int kNBars = 4 + 2 * kQStages + 8;
   static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;
 };
@@ -223,23 +232,27 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const bool active = run0 + (2 * pr + w) * kKeys < sq.len;
         ok = bar_wait(bar_kf + 8 * (pr & 1), (uint32_t)(pr / 2) & 1u, abort);
         for (int i = q_first(pr); i < nq && ok; i += p.split) {
-          const int s = resident ? i : taken % kQStages, b = 2 * w + (n_s & 1);
+          const int s = resident ? i : taken % kQStages;
           ok = bar_wait(bar_qf + 8 * s, resident ? 0u : (uint32_t)(taken / kQStages) & 1u, abort);
           ++taken;
           if (ok && active) {
-            if (n_s > 1 && !(ok = bar_wait(bar_se + 8 * b, (uint32_t)(n_s / 2 - 1) & 1u, abort))) break;
-            tm_fence_after();
             const uint64_t da = sw128_desc(sbase + k_tile(pr, w), 0), db = sw128_desc(sbase + q_tile(s), 0);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
-              if (one) mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > 0);
+            for (int half = 0; half < 2; ++half) {
+              const int b = 2 * w + half;
+              if (n_s > 0 && !(ok = bar_wait(bar_se + 8 * b, (uint32_t)(n_s - 1) & 1u, abort))) break;
+              tm_fence_after();
+#pragma unroll
+              for (int ks = half * D / 32; ks < (half + 1) * D / 32; ++ks) {
+                const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
+                if (one) mma_ss(tm + 128 * b, da + off, db + off, idesc, ks > half * D / 32);
+              }
+              if (one && half)
+                mma_ss(tm + 128 * b, plain_desc(sbase + L::kOnes, 2048),
+                       plain_desc(sbase + L::kL + s * 2048, L::kZero - L::kL - s * 2048), idesc, 1);
+              if (one) mma_commit(bar_sf + 8 * b);
             }
-            if (one) {
-              mma_ss(tm + 128 * b, plain_desc(sbase + L::kOnes, 2048),
-                     plain_desc(sbase + L::kL + s * 2048, L::kZero - L::kL - s * 2048), idesc, 1);
-              mma_commit(bar_sf + 8 * b);
-            }
+            if (!ok) break;
             ++n_s;
           }
           if (ok && one && !resident) mma_commit(bar_qe + 8 * s);
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (one && p.status) atomicOr(p.status, kStatusPromptTimeout);
       }
       // nothing in flight when the CTA ends
-      for (int x = max(0, n_s - 2); x < n_s; ++x) bar_drain(bar_sf + 8 * (2 * w + (x & 1)), (uint32_t)(x / 2) & 1u);
+      for (int half = 0; half < 2 && n_s > 0; ++half) bar_drain(bar_sf + 8 * (2 * w + half), (uint32_t)(n_s - 1) & 1u);
     }
   } else {
     // ============ sums: key tile w, one key a thread ==================================
@@ -266,25 +279,30 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const bool active = tile_key < sq.len;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int i = q_first(pr); i < nq && active; i += p.split) {
-        const int b = 2 * w + (n_s & 1);
-        if (!(ok = warp_wait(bar_sf + 8 * b, (uint32_t)(n_s / 2) & 1u, abort))) break;
-        ++n_s;
+        const uint32_t parity = (uint32_t)n_s++ & 1u, ts = tm + 256 * w + lanes;
+        if (!(ok = warp_wait(bar_sf + 16 * w, parity, abort))) break;
+        tm_fence_after();
+        float x0[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tm_ld32(ts + 32 * c, x0 + 32 * c);
+        tm_wait_ld();
+        tm_fence_before();
+        warp_arrive(bar_se + 16 * w);
+        if (!(ok = warp_wait(bar_sf + 16 * w + 8, parity, abort))) break;
         tm_fence_after();
         // rows [lo, hi) of the tile count for this key
         const int pos0 = tok0 + i * tile_tok;
         const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
-        const uint32_t ts = tm + 128 * b + lanes;
         auto add_tile = [&](auto with_mask) {
-          float x[2][32];
-          tm_ld32(ts, x[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
+            float x[32];
+            tm_ld32(ts + 128 + 32 * c, x);
             tm_wait_ld();
-            if (c < 3) tm_ld32(ts + 32 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float2 y = mul2(make_float2(x[c & 1][e], x[c & 1][e + 1]), sc);
+              float2 y = mul2(add2(make_float2(x[e], x[e + 1]), make_float2(x0[32 * c + e], x0[32 * c + e + 1])), sc);
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               if (decltype(with_mask)::value) {
@@ -299,7 +317,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (masked) add_tile(std::true_type());
         else add_tile(std::false_type());
         tm_fence_before();
-        warp_arrive(bar_se + 8 * b);
+        warp_arrive(bar_se + 16 * w + 8);
       }
       if (!ok) break;
       sum[0] = add2(sum[0], sum[1]);

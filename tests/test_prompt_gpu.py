@@ -280,6 +280,15 @@ def test_evict(torch, kvq, lens, keep, first, recent, dtype, d):
     check_evict(torch, kvq, k, v, w, lens, keep, first, recent)
 
 
+@pytest.mark.parametrize("lens,hkv,keep", [([1000003], 1, 5001), ([57001] * 80, 2, 300), ([20000, 9000, 33], 3, 7000)])
+def test_evict_long_runs_and_many_units(torch, kvq, lens, hkv, keep):
+    """Runs longer than shared memory holds (in a cluster and alone), and clusters of several sizes."""
+    _, k, v = inputs(torch, sum(lens), hkv, hkv, 16, "bfloat16", 15)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.exp(2 * torch.randn(hkv, sum(lens), generator=g, device="cuda")).bfloat16().float()
+    check_evict(torch, kvq, k, v, w, lens, keep, 1, 5)
+
+
 def test_evict_equal_and_special_weights(torch, kvq):
     n = 3000
     _, k, v = inputs(torch, n, 4, 4, 64, "bfloat16", 10)
