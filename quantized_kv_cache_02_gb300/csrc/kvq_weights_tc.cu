@@ -23,16 +23,18 @@
 // multiplication, one exponential and one addition, and no load of its own.
 // (Read per column from shared memory instead, the loads took the bandwidth that
 // the MMAs' operands need: 123 us, then 80 us, for 4096 whole tokens, 32/8 heads
-// of 128; 64 us with a MMA warp a tile and no more CTAs a pair than fill the SMs.)
+// of 128; 63 us with a MMA warp a tile and no more CTAs a pair than fill the SMs.)
 //
 // A score is two sums, over the first and the last half of the channels, added by
 // the thread: the tensor cores round every accumulation toward zero, by more the
 // larger the sum, and four steps of half the size lose less than half of eight.
-// The thread holds the first half in registers, so its buffer fills with the next
-// tile's while this tile's second half is read.
+// It adds them before anything else, so both buffers fill with the next tile's
+// during this one's exponentials.  This costs 12 us of the 75 us above's case now
+// takes and makes the weights about twice as exact (1.6e-6 to 0.9e-6 at worst).
 //
 // Bound: per pair and query tile 9/8 of 1024 cycles of MMA and 1024 of
-// exponentials on each scheduler; measured, about 1500 of both together.
+// exponentials on each scheduler; measured, some 1800 of both and the additions
+// together.
 // ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d) + M).)
 
 #include <algorithm>
@@ -46,7 +48,7 @@ namespace {
 
 constexpr int kKeys = 128, kRows = 128;
 constexpr int kMmaWarp = 8, kCopyWarp = 10, kWThreads = 384;  // MMA warps 8 and 9; 11 only fills the warpgroup
-constexpr int kSumRegs = 200, kOtherRegs = 104;              // a thread, out of the launch's 3 x 168
+constexpr int kSumRegs = 216, kOtherRegs = 72;              // a thread, out of the launch's 3 x 168
 constexpr int kQStages = 4, kStayTiles = 2;
 
 template <int D>
@@ -282,42 +284,47 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const uint32_t parity = (uint32_t)n_s++ & 1u, ts = tm + 256 * w + lanes;
         if (!(ok = warp_wait(bar_sf + 16 * w, parity, abort))) break;
         tm_fence_after();
-        float x0[128];
+        float x[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tm_ld32(ts + 32 * c, x0 + 32 * c);
+        for (int c = 0; c < 4; ++c) tm_ld32(ts + 32 * c, x + 32 * c);
         tm_wait_ld();
         tm_fence_before();
         warp_arrive(bar_se + 16 * w);
         if (!(ok = warp_wait(bar_sf + 16 * w + 8, parity, abort))) break;
         tm_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float y[32];
+          tm_ld32(ts + 128 + 32 * c, y);
+          tm_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 z = add2(make_float2(x[32 * c + e], x[32 * c + e + 1]), make_float2(y[e], y[e + 1]));
+            x[32 * c + e] = z.x;
+            x[32 * c + e + 1] = z.y;
+          }
+        }
+        tm_fence_before();
+        warp_arrive(bar_se + 16 * w + 8);
         // rows [lo, hi) of the tile count for this key
         const int pos0 = tok0 + i * tile_tok;
         const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
         auto add_tile = [&](auto with_mask) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float x[32];
-            tm_ld32(ts + 128 + 32 * c, x);
-            tm_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 y = mul2(add2(make_float2(x[e], x[e + 1]), make_float2(x0[32 * c + e], x0[32 * c + e + 1])), sc);
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              if (decltype(with_mask)::value) {
-                const int r = 32 * c + e;
-                y.x = r >= lo && r < hi ? y.x : 0.f;
-                y.y = r + 1 >= lo && r + 1 < hi ? y.y : 0.f;
-              }
-              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+          for (int r = 0; r < kRows; r += 2) {
+            float2 y = mul2(make_float2(x[r], x[r + 1]), sc);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            if (decltype(with_mask)::value) {
+              y.x = r >= lo && r < hi ? y.x : 0.f;
+              y.y = r + 1 >= lo && r + 1 < hi ? y.y : 0.f;
             }
+            sum[(r >> 1) & 1] = add2(sum[(r >> 1) & 1], y);
           }
         };
         if (masked) add_tile(std::true_type());
         else add_tile(std::false_type());
-        tm_fence_before();
-        warp_arrive(bar_se + 16 * w + 8);
       }
       if (!ok) break;
       sum[0] = add2(sum[0], sum[1]);
