@@ -281,6 +281,7 @@ kvq_status prompt_weights(const kvq_prompt* p, const void* q, const void* k, con
   // Unraised and of whole scores the weights of a 4096-token prompt were 4.5e-6
   // off, raised 1.1e-6; so, 0.8e-6.
   set_scale(p, tensor_cores(p) ? rounding_loss((p->head_dim / 32 + 1) / 2.0 - 0.25) : 0.0, &pp);
+  pp.split = 1;
   const bool tc = tensor_cores(p);
   int n_sm = 0;
   if (tc) KVQ_TRY(sm_count(&n_sm));
