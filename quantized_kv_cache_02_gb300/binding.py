@@ -416,7 +416,7 @@ def prompt_weights(q, k, lse, seq_lens, last, out=None):
     p.queries(q)
     p.rows("lse", lse, q.shape[1])
     out = p.rows("out", out, p.heads)
-    p.call(load_library().kvq_prompt_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(), last, out.data_ptr())
+    p.call(load_library().kvq_prompt_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(), int(last), out.data_ptr())
     return out
 
 
@@ -455,7 +455,7 @@ def evict(k, v, weights, seq_lens, keep, first=0, recent=0):
     v_out = torch.empty_like(k_out)
     index = torch.empty(rows, dtype=torch.int32, device=device)
     p.call(load_library().kvq_evict, k.data_ptr(), v.data_ptr(), weights.data_ptr(),
-           _counts(counts), first, recent, k_out.data_ptr(), v_out.data_ptr(),
+           _counts(counts), int(first), int(recent), k_out.data_ptr(), v_out.data_ptr(),
            index.data_ptr())
     return Kept(k_out, v_out, index, counts, p.heads)
 
@@ -527,7 +527,14 @@ class KVQCache:
         kvq_append(self.handle, new_k.data_ptr(), new_v.data_ptr(), n, seq_begin, n_seqs, self._stream())
 
     def append_kept(self, kept, seq_begin=0):
-        """Append what evict kept: its sequence i to sequence seq_begin + i."""
+        """Append what evict kept: its sequence i to sequence seq_begin + i.
+        Lengths are checked for all of them before the first is appended."""
+        assert 0 <= seq_begin and seq_begin + len(kept.counts) <= self.cfg.batch, \
+            f"{len(kept.counts)} sequences from {seq_begin} on do not fit a batch of {self.cfg.batch}"
+        for i, n in enumerate(kept.counts):
+            held = self.seq_state(seq_begin + i)["total"]
+            if held + n > self.capacity[seq_begin + i]:
+                raise KVQError(KVQ_ECAPACITY, f"sequence {seq_begin + i}: {held} + {n} tokens exceed its capacity")
         for i, n in enumerate(kept.counts):
             if n:
                 k, v, _ = kept.sequence(i)

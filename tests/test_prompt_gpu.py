@@ -345,6 +345,44 @@ def test_streams_and_graphs(torch, kvq):
     assert kvq.prompt_status() == 0
 
 
+@pytest.mark.parametrize("d", [128, 48])
+def test_c_entry_without_lse_and_status(torch, kvq, d):
+    q, k, v = inputs(torch, 150, 4, 2, d, "bfloat16", 16)
+    want, _ = kvq.prompt_attention(q, k, v, [150])
+    out = torch.zeros_like(q)
+    p = kvq.binding._Prompt(k, [150])
+    p.queries(q)
+    p.values(v)
+    p.c.out_token_stride, p.c.out_head_stride = out.stride()[:2]
+    p.c.status = None
+    before = kvq.kvq_kernel_launches()
+    kvq.kvq_prompt_attention(p.c, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None,
+                             torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(out, want) and kvq.kvq_kernel_launches() == before + 1
+
+
+def test_integers_of_other_kinds(torch, kvq):
+    q, k, v = inputs(torch, 60, 2, 2, 64, "bfloat16", 17)
+    lens = np.array([40, 20])
+    out, lse = kvq.prompt_attention(q, k, v, lens)
+    assert torch.equal(out, kvq.prompt_attention(q, k, v, [40, 20])[0])
+    w = kvq.prompt_weights(q, k, lse, torch.tensor([40, 20]), np.int64(8))
+    kept = kvq.evict(k, v, w, lens, np.int32(16), np.int64(1), np.int64(2))
+    plain = kvq.evict(k, v, w, [40, 20], [16, 16], 1, 2)
+    assert kept.counts == plain.counts and torch.equal(kept.index, plain.index)
+
+
+def test_append_kept_checks_before_it_appends(torch, kvq):
+    _, k, v = inputs(torch, 200, 2, 2, 64, "bfloat16", 18)
+    kept = kvq.evict(k, v, torch.rand(2, 200, device="cuda"), [100, 100], [30, 80])
+    cache = kvq.KVQCache(2, 2, 2, 64, 16, 8, 7, 64)
+    with pytest.raises(kvq.KVQError):
+        cache.append_kept(kept)
+    assert cache.seq_state(0)["total"] == 0
+    with pytest.raises(AssertionError):
+        cache.append_kept(kept, 1)
+
+
 def test_tensor_refusals(torch, kvq):
     q, k, v = inputs(torch, 40, 8, 2, 64, "bfloat16", 13)
     lse = torch.zeros(8, 40, device="cuda")
