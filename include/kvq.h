@@ -445,10 +445,11 @@ kvq_status kvq_compare(const void* key, const void* value, int64_t batch, int32_
  * q, out: [n_tokens][n_q_heads][head_dim]; k, v: [n_tokens][n_kv_heads]
  * [head_dim]; lse: float [n_q_heads][n_tokens] (natural logarithm; may be
  * NULL).  Scores, softmax statistics and the output sum are fp32; for bf16 the
- * softmax weights are rounded to bf16 before they meet v.  One sequence's
- * values never reach another's result, whatever they hold; inside a sequence
- * finite values are assumed (as everywhere in this library), Values small enough
- * for fp32 sums of 2^8 times their size.  out must not overlap the inputs, nor
+ * softmax weights are rounded to bf16 before they meet v.  Nothing of another
+ * sequence or of a later token reaches a result, infinities and NaN included;
+ * an infinite or NaN element of v makes that element of the tokens from its own
+ * on infinite or NaN.  Finite Values are to be small enough for fp32 sums of 2^8
+ * times their size.  out must not overlap the inputs, nor
  * its rows each other.  No gradient: like the rest of the library this serves
  * inference.  Only enqueues work on ``stream``; needs no workspace, and
  * two calls may run at once.  Errors before any launch: KVQ_EINVAL (shape,

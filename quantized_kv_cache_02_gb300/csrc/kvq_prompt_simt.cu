@@ -46,18 +46,27 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
 // Rows [0, 64) of K or V (keys ``key0`` on of one head) into shared memory as
 // fp32 rows of ``stride`` floats; keys at or past ``end`` and channels past D are 0.
-template <typename T>
-__device__ __forceinline__ void load_keys(float* dst, int stride, int cols, const T* base, int64_t ts, int key0,
+// CLEAN: infinities and NaN too; returns whether there were any.
+template <bool CLEAN, typename T>
+__device__ __forceinline__ bool load_keys(float* dst, int stride, int cols, const T* base, int64_t ts, int key0,
                                           int end, int D) {
+  bool dirty = false;
   const int per = cols / 4;
   for (int i = threadIdx.x; i < kPromptKeys * per; i += kThreads) {
     const int r = i / per, c = (i - r * per) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (key0 + r < end && c < D) x = load4(base + (int64_t)(key0 + r) * ts + c);
+    if (CLEAN && !(finite(x.x) && finite(x.y) && finite(x.z) && finite(x.w))) {
+      dirty = true;
+      x = make_float4(finite(x.x) ? x.x : 0.f, finite(x.y) ? x.y : 0.f, finite(x.z) ? x.z : 0.f, finite(x.w) ? x.w : 0.f);
+    }
     *reinterpret_cast<float4*>(dst + r * stride + c) = x;
   }
+  return dirty;
 }
 
 // Row r of a query tile is token tok0 + r / g, head h * g + r % g; rows past
@@ -158,9 +167,10 @@ __global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(
 #pragma unroll
     for (int c = 0; c < NC; ++c) o[c][i][0] = o[c][i][1] = make_float2(0.f, 0.f);
   }
+  int dirty = 0;
   for (int k0 = rank * kPromptKeys; k0 < end; k0 += p.split * kPromptKeys) {
     __syncthreads();  // the previous step's V has been read
-    load_keys(ks, kStride, p.D, k, p.k_ts, k0, end, p.D);
+    load_keys<false>(ks, kStride, p.D, k, p.k_ts, k0, end, p.D);
     __syncthreads();
     float s[4][4];
     scores(s, qs, ks, kStride, p.D, ty, tx);
@@ -194,8 +204,13 @@ __global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(
       }
     }
     __syncthreads();  // K has been read; P is complete
-    load_keys(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D);
-    __syncthreads();
+    // A weight of 0 does not silence an infinite or NaN Value: in blocks with keys
+    // that some row does not see they are taken out, and given back at the end.
+    if (k0 + kPromptKeys - 1 > tok0) dirty |= __syncthreads_or(load_keys<true>(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D));
+    else {
+      load_keys<false>(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D);
+      __syncthreads();
+    }
 #pragma unroll 2
     for (int n = 0; n < kPromptKeys; n += 4) {
       float4 pr[4];
@@ -220,6 +235,25 @@ __global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
     for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+  }
+  if (dirty) {
+    // a weight times an infinity or NaN is one
+    for (int key = tok0 / kPromptKeys * kPromptKeys; key < end; ++key) {
+      if (key / kPromptKeys % p.split != rank) continue;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (64 * c + 4 * tx >= p.D) continue;
+        const float4 x = load4(v + (int64_t)key * p.v_ts + 64 * c + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (key > pos[i]) continue;
+          if (!finite(x.x)) o[c][i][0].x += x.x;
+          if (!finite(x.y)) o[c][i][0].y += x.y;
+          if (!finite(x.z)) o[c][i][1].x += x.z;
+          if (!finite(x.w)) o[c][i][1].y += x.w;
+        }
+      }
+    }
   }
   auto finish = [&](int r, int col, float4 sum, float mr, float lr, bool first) {  // row r, columns col .. col + 3
     const int t = r / p.g, head = h * p.g + r - t * p.g;
@@ -293,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_con
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   pdl_wait();
   pdl_release();
-  load_keys(ks, stride, p.D, k, p.k_ts, k0, sq.len, p.D);
+  load_keys<false>(ks, stride, p.D, k, p.k_ts, k0, sq.len, p.D);
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   const int64_t back = sq.len - p.last;
   const int t_first = (int)(back > k0 ? back : k0);

@@ -12,10 +12,11 @@
 //
 // Warps 0-3 and 4-7 run the softmax of tile 0 and 1, one row a thread, so
 // maxima and sums need no exchange; warp 8 issues the MMAs, warp 9 the TMA
-// copies.  At d = 128 tensor memory holds S, with P over it, and O: the tiles
-// alternate, one's MMAs run under the other's softmax.  At d = 64 P has columns
-// of its own, S_i is free once its rows are in registers, and the next block's
-// Q K^T runs under the same tile's softmax too.
+// copies, and with 10 and 11 it cleans the Values that some row does not see.
+// At d = 128 tensor memory holds S, with P over it, and O: the tiles alternate,
+// one's MMAs run under the other's softmax.  At d = 64 P has columns of its own,
+// S_i is free once its rows are in registers, and the next block's Q K^T runs
+// under the same tile's softmax too.
 //
 // Bound at d = 128: the MMAs, 2048 cycles for two tiles and a block, measured
 // some 2600 with the waits between them: 4096 tokens of 32/8 heads 96 us (1.43
@@ -30,6 +31,8 @@
 // threads themselves.
 // ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d) + M) V.)
 
+#include <cfloat>
+
 #include "kvq_prompt.h"
 #include "kvq_tcgen05.cuh"
 
@@ -37,7 +40,7 @@ namespace kvq {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kTcThreads = 384;  // warps 10 and 11 only fill the third warpgroup
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kTcThreads = 384;
 // Registers a thread after the split of the launch's 3 x 168: a softmax thread
 // holds a whole row of scores.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
@@ -49,13 +52,39 @@ struct TcLayout {
   static constexpr uint32_t kChunk = 128 * 128;           // 128 rows of 64 channels
   static constexpr uint32_t kTile = kChunk * (D / 64);    // a Q, K or V tile
   static constexpr uint32_t kQ = 0, kK0 = 2 * kTile, kRing = 3 * kTile, kBars = kRing + 2 * kSlots * kTile;
-  // barriers: full and empty per slot, K_0, the cleared Value rows, then per tile: Q, S, P (two halves), O, S read
-  static constexpr int kNBars = 2 * kSlots + 2 + 12;
+  // barriers: full and empty per slot, K_0, cleaned Values (two), then per tile: Q, S, P (two halves), O, S read
+  static constexpr int kNBars = 2 * kSlots + 3 + 12;
   static constexpr bool kApart = D == 64;                 // P beside S, not over it
-  static constexpr size_t kSmem = kBars + kNBars * 8 + 16 + 1024;  // + alignment
+  static constexpr size_t kSmem = kBars + kNBars * 8 + 32 + 1024;  // + alignment
   // S_i at 128 i, O_i at 256 + D i, P_i over S_i or at 384 + 64 i
   static constexpr uint32_t kColS = 0, kColO = 256, kColP = kApart ? 384 : 0, kStepP = kApart ? 64 : 128;
 };
+
+__device__ __forceinline__ __nv_bfloat162 times_zero(uint32_t w, __nv_bfloat162 sum) {
+  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __nv_bfloat162{}, sum);
+}
+
+// The infinities and NaN that were taken out, to the rows that see them: a weight
+// times one is one.  (By the softmax warps; all rows have been written.)
+template <int D>
+__device__ __forceinline__ void give_back(const PromptParams& p, int si, int h, int level) {
+  const PromptSeq sq = p.tiles.seq[si];
+  const int tok0 = level * p.tiles.step, end = min(sq.len, tok0 + p.tiles.step), lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < (end - tok0) * p.g; r += kMmaWarp) {
+    const int pos = tok0 + r / p.g;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(sq.start + pos) * p.o_ts +
+                         (int64_t)(h * p.g + r % p.g) * p.o_hs;
+    for (int c = lane; c < D; c += 32) {
+      float o = __bfloat162float(dst[c]);
+      for (int key = tok0 + 1; key <= pos; ++key) {
+        const float x = __bfloat162float(
+            static_cast<const __nv_bfloat16*>(p.v)[(int64_t)(sq.start + key) * p.v_ts + (int64_t)h * p.v_hs + c]);
+        if (!isfinite(x)) o += x;
+      }
+      dst[c] = __float2bfloat16(o);
+    }
+  }
+}
 
 struct TcMaps {
   CUtensorMap q, k, v;
@@ -70,10 +99,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kSlots;
-  const uint32_t bar_k0 = bar_empty + 8 * L::kSlots, bar_clear = bar_k0 + 8, bar_q = bar_clear + 8, bar_s = bar_q + 16,
+  const uint32_t bar_k0 = bar_empty + 8 * L::kSlots, bar_clean = bar_k0 + 8, bar_q = bar_clean + 16, bar_s = bar_q + 16,
                  bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* dirty = abort + 1;  // then the tile, kept here and not in registers
 
   int si, h, level;
   prompt_tile(p.tiles, blockIdx.x, &si, &h, &level);
@@ -84,11 +114,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int end0 = min(sq.len, tok0 + tile_tok), end1 = min(sq.len, tok0 + 2 * tile_tok);
   const int n0 = (end0 + kKeys - 1) / kKeys, n1 = tok0 + tile_tok < sq.len ? (end1 + kKeys - 1) / kKeys : 0;
   const int nmax = max(n0, n1);
-  // Value rows of the last block past the sequence hold other sequences'
-  // values, and a weight of 0 does not silence a NaN there: the ones that the
-  // last k-step of 16 covers are cleared
-  const int valid = sq.len - (nmax - 1) * kKeys;
-  const bool clear = valid < kKeys && (valid & 15) != 0;
+  // A weight of 0 does not silence an infinite or NaN Value.  Blocks from
+  // ``own`` on (two at most) hold Values that some row does not see: later
+  // tokens', whose infinities and NaN are taken out and given back at the end to
+  // the rows that see them, and in a last k-step of 16 other sequences', cleared.
+  const int own = tok0 / kKeys;
 
   // the copies: Q_0, K_0, Q_1, then the pairs V_j, K_j+1
   auto load_q = [&](int i) {
@@ -113,13 +143,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (t == 32 * kCopyWarp) {
     // the first copies fly while the rest of the CTA sets up
     *abort = 0;
+    *dirty = 0;
+    dirty[1] = si;
+    dirty[2] = h;
+    dirty[3] = level;
     for (int s = 0; s < L::kSlots; ++s) {
       bar_init(bar_full + 8 * s, 1);
       bar_init(bar_empty + 8 * s, 1);
     }
     bar_init(bar_k0, 1);
-    bar_init(bar_clear, 1);
     for (int i = 0; i < 2; ++i) {
+      bar_init(bar_clean + 8 * i, 3);
       bar_init(bar_q + 8 * i, 1);
       bar_init(bar_s + 8 * i, 1);
       bar_init(bar_p + 16 * i, 4);  // a warp arrives once, by one lane
@@ -144,9 +178,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    int issued = 0;
     if (warp == kCopyWarp) {
       // ============ copies (lane 0) ==================================================
-      int issued = min(nmax, L::kSlots);
+      issued = min(nmax, L::kSlots);
       if (lane == 0) {
         for (; issued < nmax; ++issued) {
           if (!bar_wait(bar_empty + 8 * (issued % L::kSlots), (uint32_t)(issued / L::kSlots - 1) & 1u, abort)) {
@@ -159,22 +194,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       issued = __shfl_sync(0xffffffffu, issued, 0);
       // nothing in flight when the CTA ends
-      for (int x = max(0, issued - L::kSlots); x < issued; ++x)
+      for (int x = max(0, issued - L::kSlots); x < min(issued, own); ++x)
         bar_drain(bar_full + 8 * (x % L::kSlots), (uint32_t)(x / L::kSlots) & 1u);
-      if (clear && issued == nmax) {
-        uint8_t* v = smem + L::kRing + 2 * ((nmax - 1) % L::kSlots) * L::kTile;
-        const int n = (16 - (valid & 15)) * 8;  // 16-byte pieces of a chunk
-        for (int x = lane; x < n * (D / 64); x += 32) {
-          const int c = x / n, y = x - c * n;
-          *reinterpret_cast<uint4*>(v + c * L::kChunk + valid * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (warp >= kCopyWarp) {
+      // ============ Values that some row does not see (keys past tok0 that a k-step
+      // of a tile covers), by the three warps that issue no MMA, under the softmax: the
+      // check costs 0.7 us of a short call, nothing at 4096 tokens.  (After an early
+      // stop this runs on whatever is there.)
+      for (int j = own; j < nmax; ++j) {
+        if (warp == kCopyWarp && j < issued) bar_drain(bar_full + 8 * (j % L::kSlots), (uint32_t)(j / L::kSlots) & 1u);
+        asm volatile("bar.sync 1, 96;" ::: "memory");  // the copy warp has seen it land
+        const int mine = t - 32 * kCopyWarp;
+        uint8_t* v = smem + L::kRing + 2 * (j % L::kSlots) * L::kTile;
+        const int len = min(sq.len - j * kKeys, kKeys), first = max(0, tok0 + 1 - j * kKeys);
+        const int last = min(len, ((n1 > 0 ? end1 : end0) - j * kKeys + 15) & ~15);
+        __nv_bfloat162 sum[2] = {};  // NaN once an infinity or a NaN came
+        for (int c = 0; c < D / 64; ++c) {
+          uint4* rows = reinterpret_cast<uint4*>(v + c * L::kChunk);
+          for (int x = 8 * len + mine; x < 8 * ((len + 15) & ~15); x += 96) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+          for (int x = 8 * first + mine; x < 8 * last; x += 96) {
+            const uint4 w = rows[x];
+            sum[0] = times_zero(w.x, sum[0]);
+            sum[1] = times_zero(w.y, sum[1]);
+            sum[0] = times_zero(w.z, sum[0]);
+            sum[1] = times_zero(w.w, sum[1]);
+          }
+        }
+        const float2 any = __bfloat1622float2(__hadd2(sum[0], sum[1]));
+        if (any.x + any.y != 0.f) {
+          auto finite = [](uint32_t w) {
+            return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) |
+                   ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+          };
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t* words = reinterpret_cast<uint32_t*>(v + c * L::kChunk);
+#pragma unroll 1
+            for (int x = 8 * first + mine; x < 8 * last; x += 96)
+#pragma unroll 1
+              for (int y = 0; y < 4; ++y) words[4 * x + y] = finite(words[4 * x + y]);
+          }
+          *dirty = 1;
         }
         async_proxy_fence();
-        warp_arrive(bar_clear);
+        warp_arrive(bar_clean + 8 * (j - own));
       }
-      bar_drain(bar_k0, 0);
-      bar_drain(bar_q, 0);
-      if (n1 > 0) bar_drain(bar_q + 8, 0);
-    } else if (warp == kMmaWarp) {
+      if (warp == kCopyWarp) {
+        bar_drain(bar_k0, 0);
+        bar_drain(bar_q, 0);
+        if (n1 > 0) bar_drain(bar_q + 8, 0);
+      }
+    } else {
       // ============ MMAs, all issued by one lane ======================================
       // The MMAs run in the order of issue.  With P over S, Q K^T of the next
       // block may therefore overwrite P right behind the P V that reads it, and
@@ -204,7 +275,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int j = 0; j < nmax && ok; ++j) {
         const int s = j % L::kSlots;
         const uint32_t vaddr = sbase + L::kRing + 2 * s * L::kTile, kaddr = vaddr + L::kTile;
-        if (clear && j == nmax - 1) ok = bar_wait(bar_clear, 0, abort);
         if (L::kApart) {
           for (int i = 0; i < 2 && ok; ++i) {
             if (j + 1 >= (i ? n1 : n0)) continue;
@@ -223,6 +293,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             j > 0 || ks > 0);
           };
           if (!(ok = bar_wait(bar_p + 16 * i, (uint32_t)j & 1u, abort))) break;
+          if (j >= own && !(ok = bar_wait(bar_clean + 8 * (j - own), 0, abort))) break;
           tm_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
@@ -261,7 +332,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t ts = tm + L::kColS + 128 * i + lanes, to = tm + L::kColO + D * i + lanes,
                    tp = tm + L::kColP + L::kStepP * i + lanes;
     const float2 sc = make_float2(p.scale2, p.scale2);
-    float m = -INFINITY, l = 0.f;
+    float m = -FLT_MAX, l = 0.f;  // (not -INFINITY: scores of minus infinity may come first)
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       if (!(ok = warp_wait(bar_s + 8 * i, (uint32_t)j & 1u, abort))) break;
@@ -386,6 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
     tm_free<512>(tm);
   }
+  if (warp < kMmaWarp && *dirty) give_back<D>(p, dirty[1], dirty[2], dirty[3]);
 }
 
 template <int D>

@@ -155,6 +155,63 @@ def test_other_sequences_and_rows_behind_the_last_stay_out(torch, kvq, d, dtype)
         check_weights(torch, w[:, s], q[s], k[s], lse[:, s], [n], 64)
 
 
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (2, 2), (5, 1)])
+@pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "bfloat16"), (96, "bfloat16"), (256, "bfloat16"),
+                                     (128, "float32")])
+def test_infinities_and_nan_of_later_tokens_stay_out(torch, kvq, d, dtype, hq, hkv):
+    """A Value reaches the tokens from its own on: infinities and NaN make those
+    elements infinite or NaN and leave every other bit as zeros in their place do."""
+    lens = [700, 70, 1]
+    q, k, v = inputs(torch, sum(lens), hq, hkv, d, dtype, 11)
+    bad = torch.zeros(v.shape, device="cuda")
+    for token, channel, x in ((3, 5, math.inf), (130, 2, math.nan), (131, 3, -math.inf), (150, 3, math.inf),
+                              (300, slice(16, 32), math.inf), (301, 17, -math.inf), (555, 0, math.nan),
+                              (556, slice(40, 48), -math.inf), (690, d - 1, math.inf), (699, slice(0, d), math.nan),
+                              (700, 7, math.inf), (740, 8, math.nan), (769, 9, -math.inf)):
+        bad[token, hkv - 1, channel] = x
+    v = torch.where(bad != 0, torch.zeros_like(v), v)
+    want, lse = kvq.prompt_attention(q, k, v, lens)
+    check_attention(torch, want, lse, q, k, v, lens)
+    got, l2 = kvq.prompt_attention(q, k, torch.where(bad != 0, bad.to(v.dtype), v), lens)
+    at = 0
+    for n in lens:
+        seen = bad[at:at + n].cumsum(0).repeat_interleave(hq // hkv, 1)  # infinite or NaN from the first one on
+        expect = torch.where(seen == 0, want[at:at + n].float(), seen)
+        assert torch.equal(got[at:at + n].float().nan_to_num(nan=1e30), expect.nan_to_num(nan=1e30))
+        at += n
+    assert torch.equal(lse, l2) and kvq.prompt_status() == 0
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "bfloat16"), (96, "bfloat16"), (128, "float32")])
+def test_infinities_and_nan_of_keys_and_queries(torch, kvq, d, dtype):
+    """A key counts from its token on, a query at its own row; a score of minus infinity weighs nothing."""
+    n, hq, hkv = 500, 4, 2
+    q, k, v = inputs(torch, n, hq, hkv, d, dtype, 12)
+    want, lse = kvq.prompt_attention(q, k, v, [n])
+    k2, q2 = k.clone(), q.clone()
+    k2[333, 1], q2[77, 0] = math.nan, math.nan
+    got, l2 = kvq.prompt_attention(q2, k2, v, [n])
+    rows = torch.zeros(n, hq, dtype=torch.bool, device="cuda")
+    rows[333:, 2:] = True
+    rows[77, 0] = True
+    assert got[rows].isnan().all() and torch.equal(got[~rows], want[~rows])
+    assert l2.T[rows].isnan().all() and torch.equal(l2.T[~rows], lse.T[~rows])
+    # the weights that the last queries give: a NaN query reaches the keys up to its own, a NaN key itself
+    w = kvq.prompt_weights(q, k, lse, [n], 450)
+    w2 = kvq.prompt_weights(q2, k2, lse, [n], 450)
+    nan = torch.zeros(hkv, n, dtype=torch.bool, device="cuda")
+    nan[0, :78] = True
+    nan[1, 333] = True
+    assert w2[nan].isnan().all() and torch.equal(w2[~nan], w[~nan])
+    # the first 260 keys at minus infinity for queries of positive first channel
+    q, k = q.clone(), k.clone()
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    k[:260, :, 0] = -math.inf
+    got, lse = kvq.prompt_attention(q, k, v, [n])
+    check_attention(torch, got[260:], lse[:, 260:], q[260:], k[260:], v[260:], [n - 260])
+    assert got[:260].isnan().all() and kvq.prompt_status() == 0
+
+
 @pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "bfloat16"), (96, "float32")])
 def test_strides(torch, kvq, d, dtype):
     """Slices of one fused projection, head-major tensors, a strided output, one head out of many."""
