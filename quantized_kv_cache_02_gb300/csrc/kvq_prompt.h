@@ -84,6 +84,17 @@ struct EvictParams {
   EvictSeq seq[kMaxSeqsPerLaunch];
 };
 
+// A sum that keeps what its additions round off (Kahan, "Further remarks on
+// reducing truncation errors", 1965): thousands of tiles may meet in one weight.
+struct RunningSum {
+  float sum, rest;
+  __device__ __forceinline__ void add(float x) {
+    const float y = __fsub_rn(x, rest), next = __fadd_rn(sum, y);
+    rest = __fsub_rn(__fsub_rn(next, sum), y);
+    sum = next;
+  }
+};
+
 // Launch with clusters of ``split`` CTAs in a row a tile.
 template <typename... Params, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(Params...), int64_t tiles, int split, int threads, size_t smem, cudaStream_t s,

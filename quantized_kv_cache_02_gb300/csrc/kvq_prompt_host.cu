@@ -277,10 +277,9 @@ kvq_status prompt_weights(const kvq_prompt* p, const void* q, const void* k, con
   pp.weights = weights;
   pp.last = last;
   // Two halves of D / 32 partial sums that grow to half the score; the second
-  // ends with lse taken off, which loses a quarter (as measured) the other way.
-  // Unraised and of whole scores the weights of a 4096-token prompt were 4.5e-6
-  // off, raised 1.1e-6; so, 0.8e-6.
-  set_scale(p, tensor_cores(p) ? rounding_loss((p->head_dim / 32 + 1) / 2.0 - 0.25) : 0.0, &pp);
+  // ends with lse taken off, which leaves about minus half the score of a heavy
+  // weight and loses the other way.
+  set_scale(p, tensor_cores(p) ? rounding_loss((p->head_dim / 32 + 1) / 2.0 - 0.5) : 0.0, &pp);
   pp.split = 1;
   const bool tc = tensor_cores(p);
   int n_sm = 0;

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_con
   pdl_wait();
   pdl_release();
   load_keys<false>(ks, stride, p.D, k, p.k_ts, k0, sq.len, p.D);
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  RunningSum total[4] = {};
   const int64_t back = sq.len - p.last;
   const int t_first = (int)(back > k0 ? back : k0);
   for (int t0 = t_first; t0 < sq.len; t0 += tile_tok) {
@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_con
     __syncthreads();
     float s[4][4];
     scores(s, qs, ks, stride, p.D, ty, tx);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * ty + i, t = r / p.g, pos = t0 + t;
@@ -349,9 +350,11 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_con
           if (k0 + tx + 16 * j <= pos) sum[j] = fmaf(exp2f(fmaf(s[i][j], p.scale2, -lse2)), f, sum[j]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) total[j].add(sum[j]);
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) red[ty * 64 + tx + 16 * j] = sum[j];
+  for (int j = 0; j < 4; ++j) red[ty * 64 + tx + 16 * j] = total[j].sum;
   __syncthreads();
   if (threadIdx.x < kPromptKeys && k0 + threadIdx.x < sq.len) {
     float w = 0.f;

@@ -29,8 +29,10 @@
 // the thread: the tensor cores round every accumulation toward zero, by more the
 // larger the sum, and four steps of half the size lose less than half of eight.
 // It adds them before anything else, so both buffers fill with the next tile's
-// during this one's exponentials.  This costs 12 us of the 75 us above's case now
-// takes and makes the weights about twice as exact (1.6e-6 to 0.9e-6 at worst).
+// during this one's exponentials.  It took 12 of the 75 us of 4096 whole tokens
+// and the error there from 1.6e-6 to 1.0e-6 of the weights; a running sum over the
+// tiles that keeps what it rounds off, no longer, takes it to 0.5e-6 (sums in
+// fp32 throughout: 0.4e-6, with single weights twice as far off as here).
 //
 // Bound: per pair and query tile 9/8 of 1024 cycles of MMA and 1024 of
 // exponentials on each scheduler; measured, some 1800 of both and the additions
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     for (int pr = 0; pr < pairs && ok; ++pr) {
       const int tile_key = run0 + pr * 2 * kKeys + w * kKeys, key = tile_key + (t & 127);
       const bool active = tile_key < sq.len;
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      RunningSum total[2] = {};
       for (int i = q_first(pr); i < nq && active; i += p.split) {
         const uint32_t parity = (uint32_t)n_s++ & 1u, ts = tm + 256 * w + lanes;
         if (!(ok = warp_wait(bar_sf + 16 * w, parity, abort))) break;
@@ -310,6 +312,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int pos0 = tok0 + i * tile_tok;
         const int lo = max(0, key - pos0) * p.g, hi = min(tile_tok, sq.len - pos0) * p.g;
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kRows);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         auto add_tile = [&](auto with_mask) {
 #pragma unroll
           for (int r = 0; r < kRows; r += 2) {
@@ -325,10 +328,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
         };
         if (masked) add_tile(std::true_type());
         else add_tile(std::false_type());
+        sum[0] = add2(sum[0], sum[1]);
+        total[0].add(sum[0].x);
+        total[1].add(sum[0].y);
       }
       if (!ok) break;
-      sum[0] = add2(sum[0], sum[1]);
-      const float mine = sum[0].x + sum[0].y;
+      const float mine = total[0].sum + total[1].sum;
       if (p.split > 1) {
         // into rank 0's shared memory (one pair a CTA; every rank runs: it arrived)
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
