@@ -90,7 +90,8 @@ struct RunningSum {
   float sum, rest;
   __device__ __forceinline__ void add(float x) {
     const float y = __fsub_rn(x, rest), next = __fadd_rn(sum, y);
-    rest = __fsub_rn(__fsub_rn(next, sum), y);
+    const float lost = __fsub_rn(__fsub_rn(next, sum), y);
+    rest = fabsf(lost) < INFINITY ? lost : 0.f;  // an infinite sum stays infinite
     sum = next;
   }
 };

@@ -213,6 +213,19 @@ def test_infinities_and_nan_of_keys_and_queries(torch, kvq, d, dtype):
 
 
 @pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "bfloat16"), (96, "float32")])
+def test_infinite_weights_stay_infinite(torch, kvq, d, dtype):
+    """A query whose weights overflow makes those of the keys it sees infinite, never NaN, whatever is added later."""
+    n, at = 900, 300
+    q, k, v = inputs(torch, n, 4, 2, d, dtype, 13)
+    lse = kvq.prompt_attention(q, k, v, [n])[1]
+    w = kvq.prompt_weights(q, k, lse, [n], n)
+    lse[0, at] = -1000.0
+    got = kvq.prompt_weights(q, k, lse, [n], n)
+    assert got[0, :at + 1].isposinf().all()
+    assert torch.equal(got[0, at + 1:], w[0, at + 1:]) and torch.equal(got[1], w[1])
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "bfloat16"), (96, "float32")])
 def test_strides(torch, kvq, d, dtype):
     """Slices of one fused projection, head-major tensors, a strided output, one head out of many."""
     lens, hq, hkv = [100, 61], 8, 2
