@@ -139,6 +139,8 @@ cudaError_t launch_weights_tc(const PromptParams& p, int64_t tiles, cudaStream_t
 bool tma_map3(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1,
               int b2);
 
+constexpr int kMaxDim = 256;  // head_dim
+
 // Rows of a CUDA-core attention tile and keys of one of its steps.
 constexpr int kPromptRows = 64, kPromptKeys = 64;
 

@@ -63,8 +63,8 @@ kvq_status check_prompt(const kvq_prompt* p, int64_t* total) {
                 p->n_kv_heads);
   if (p->n_q_heads / p->n_kv_heads > kvq::kMaxGqa)
     return fail(KVQ_EUNSUPPORTED, "query heads per KV head must be <= %d", kvq::kMaxGqa);
-  if (p->head_dim < 16 || p->head_dim > 256 || p->head_dim % 16 != 0)
-    return fail(KVQ_EUNSUPPORTED, "head_dim must be a multiple of 16 in [16, 256] (got %d)", p->head_dim);
+  if (p->head_dim < 16 || p->head_dim > kvq::kMaxDim || p->head_dim % 16 != 0)
+    return fail(KVQ_EUNSUPPORTED, "head_dim must be a multiple of 16 in [16, %d] (got %d)", kvq::kMaxDim, p->head_dim);
   if (p->dtype != KVQ_BF16 && p->dtype != KVQ_FP32) return fail(KVQ_EINVAL, "unknown dtype %d", p->dtype);
   if (!p->seq_lens) return fail(KVQ_EINVAL, "seq_lens is NULL");
   if (p->n_tokens < 0 || p->n_tokens > kMaxTokens)

@@ -364,9 +364,12 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_con
   }
 }
 
+// ``most``: the shared memory of the kernel's largest head_dim.  The limit is a
+// state of the kernel that all host threads share: set to one call's size, it
+// would refuse a larger call that another thread is about to launch.
 template <typename K>
-cudaError_t launch_sized(K kernel, size_t smem, int64_t tiles, const PromptParams& p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t launch_sized(K kernel, size_t most, size_t smem, int64_t tiles, const PromptParams& p, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, tiles, p.split, kThreads, smem, s, p);
 }
@@ -376,9 +379,9 @@ cudaError_t launch_attention_t(const PromptParams& p, int64_t tiles, cudaStream_
   auto smem = [](int nc) {
     return ((size_t)(kPromptRows + kPromptKeys) * (64 * nc + 4) + kPromptRows * kPStride) * sizeof(float);
   };
-  if (p.D <= 64) return launch_sized(prompt_simt_kernel<T, 1>, smem(1), tiles, p, s);
-  if (p.D <= 128) return launch_sized(prompt_simt_kernel<T, 2>, smem(2), tiles, p, s);
-  return launch_sized(prompt_simt_kernel<T, 4>, smem(4), tiles, p, s);
+  if (p.D <= 64) return launch_sized(prompt_simt_kernel<T, 1>, smem(1), smem(1), tiles, p, s);
+  if (p.D <= 128) return launch_sized(prompt_simt_kernel<T, 2>, smem(2), smem(2), tiles, p, s);
+  return launch_sized(prompt_simt_kernel<T, 4>, smem(4), smem(4), tiles, p, s);
 }
 
 }  // namespace
@@ -394,9 +397,9 @@ cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, 
 }
 
 cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s) {
-  const size_t smem = ((size_t)(kPromptRows + kPromptKeys) * (p.D + 4) + 16 * 64) * sizeof(float);
-  return dtype == 0 ? launch_sized(weights_simt_kernel<__nv_bfloat16>, smem, tiles, p, s)
-                    : launch_sized(weights_simt_kernel<float>, smem, tiles, p, s);
+  auto smem = [](int d) { return ((size_t)(kPromptRows + kPromptKeys) * (d + 4) + 16 * 64) * sizeof(float); };
+  return dtype == 0 ? launch_sized(weights_simt_kernel<__nv_bfloat16>, smem(kMaxDim), smem(p.D), tiles, p, s)
+                    : launch_sized(weights_simt_kernel<float>, smem(kMaxDim), smem(p.D), tiles, p, s);
 }
 
 }  // namespace kvq

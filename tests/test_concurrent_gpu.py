@@ -1,0 +1,80 @@
+"""Calls of several host threads and caches at once: what one of them asks of a
+kernel must not reach another's launch."""
+
+import ctypes
+import shutil
+import subprocess
+import threading
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+# the calls of one thread, back to back in C: Python's own lock would let the threads take turns
+CALLS = """
+#include "kvq.h"
+int weights_calls(kvq_status (*fn)(const kvq_prompt*, const void*, const void*, const float*, int64_t, float*, void*),
+                  const kvq_prompt* p, const void* q, const void* k, const float* lse, float* w, void* stream, int n) {
+  int failed = 0;
+  for (int i = 0; i < n; ++i) failed += fn(p, q, k, lse, 32, w, stream) != KVQ_OK;
+  return failed;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch
+
+
+@pytest.fixture(scope="module")
+def kvq(torch):
+    import quantized_kv_cache_02_gb300 as kvq
+    kvq.load_library()
+    return kvq
+
+
+@pytest.fixture(scope="module")
+def calls(tmp_path_factory):
+    import os
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    at = tmp_path_factory.mktemp("calls")
+    (at / "calls.c").write_text(CALLS)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([cc, "-O2", "-shared", "-fPIC", "-I", os.path.join(root, "include"), str(at / "calls.c"), "-o",
+                    str(at / "calls.so")], check=True)
+    return ctypes.CDLL(str(at / "calls.so")).weights_calls
+
+
+def test_weights_of_several_head_dims(torch, kvq, calls):
+    """The CUDA-core weights kernel serves every head_dim, each with its own shared memory."""
+    lens, threads, outs, failed = [70, 31], [], [], []
+    gate = threading.Barrier(4)
+
+    def run(p, q, k, lse, out, stream):
+        gate.wait()
+        failed.append(calls(kvq.load_library().kvq_prompt_weights, ctypes.byref(p.c), *(ctypes.c_void_p(x.data_ptr())
+                            for x in (q, k, lse, out)), ctypes.c_void_p(stream.cuda_stream), 20000))
+
+    for d in (256, 16, 256, 64):
+        q = torch.randn(sum(lens), 4, d, device="cuda")
+        k = torch.randn(sum(lens), 2, d, device="cuda")
+        lse = kvq.prompt_attention(q, k, k, lens)[1]
+        p = kvq.binding._Prompt(k, lens)
+        p.queries(q)
+        out = torch.empty(2, sum(lens), device="cuda")
+        outs.append((out, kvq.prompt_weights(q, k, lse, lens, 32)))
+        threads.append(threading.Thread(target=run, args=(p, q, k, lse, out, torch.cuda.Stream())))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0, 0, 0]
+    assert all(torch.equal(a, b) for a, b in outs)
