@@ -477,8 +477,8 @@ kvq_status create(const kvq_config* cfg, const int64_t* capacity_per_seq, int64_
     e = cudaMemset(c->range, 0, (size_t)cfg->batch * cfg->n_kv_heads * 2 * sizeof(uint32_t));
   if (e == cudaSuccess && c->done) e = cudaMemset(c->done, 0, (size_t)cfg->batch * cfg->n_kv_heads * sizeof(uint32_t));
   if (e == cudaSuccess) {
-    const size_t smem = kvq::flush_launch_smem(cfg->group, cfg->head_dim, esize_of(cfg));
-    e = kvq::configure_append(cfg->dtype, c->bits, smem);
+    // the most any cache needs: the limit is a state of the kernels that all caches share
+    e = kvq::configure_append(cfg->dtype, c->bits, kvq::kFlushSmemMax);
   }
   if (cur != attr.device) cudaSetDevice(cur);
   if (e != cudaSuccess) {

@@ -78,3 +78,17 @@ def test_weights_of_several_head_dims(torch, kvq, calls):
     torch.cuda.synchronize()
     assert failed == [0, 0, 0, 0]
     assert all(torch.equal(a, b) for a, b in outs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_second_cache_leaves_the_first_ones_appends_alone(torch, kvq, dtype):
+    """An append's shared memory goes by its cache's group and head_dim: a later cache needs less here."""
+    big = kvq.KVQCache(1, 2, 4, 128, 64, 128, 7, 512, dtype=dtype)
+    alone = kvq.KVQCache(1, 2, 4, 128, 64, 128, 7, 512, dtype=dtype)
+    k, v = (torch.randn(1, 2, 400, 128, device="cuda").to(big.dtype) for _ in range(2))
+    alone.append(k, v)
+    kvq.KVQCache(1, 2, 4, 32, 16, 8, 7, 64, dtype=dtype)
+    big.append(k, v)
+    torch.cuda.synchronize()
+    a, b = big.export_unit(0, 1), alone.export_unit(0, 1)
+    assert big.seq_state(0) == alone.seq_state(0) and all((a[x] == b[x]).all() for x in a)
