@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kvq_wait.h"
+
 namespace kvq {
 namespace {
 
@@ -38,18 +40,13 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // set by another part of the CTA that will not complete the phase.
 constexpr uint64_t kBarNanoseconds = 1000000000;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  if (bar_try(bar, parity)) return true;
-  uint64_t begun = 0;
-  for (uint32_t it = 1;; ++it) {
-    if (bar_try(bar, parity)) return true;
-    if (abort && *abort) return false;
-    if ((it & 63) == 0) {
-      uint64_t now;
-      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
-      if (begun == 0) begun = now;
-      if (now - begun > kBarNanoseconds) return false;
-    }
-  }
+  return bounded_wait([=] { return bar_try(bar, parity); }, [=] { return abort && *abort; },
+                      [] {
+                        uint64_t now;
+                        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+                        return now;
+                      },
+                      kBarNanoseconds);
 }
 // A wait that every lane of the warp leaves with the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
