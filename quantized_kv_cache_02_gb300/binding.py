@@ -19,6 +19,8 @@ KVQ_BF16, KVQ_FP32 = 0, 1
 STATUS_NAMES = {0: "KVQ_OK", 1: "KVQ_EINVAL", 2: "KVQ_ECAPACITY", 3: "KVQ_ENOMEM", 4: "KVQ_ECUDA",
                 5: "KVQ_EUNSUPPORTED", 6: "KVQ_EDEVICE"}
 
+MAX_FLUSHED_GROUPS = 4096  # of one sequence in one append to a paged cache
+
 # Every function include/kvq.h declares.
 EXPORTED = ("kvq_required_bytes", "kvq_create", "kvq_append", "kvq_decode_attention",
             "kvq_decode_attention_ex", "kvq_bytes", "kvq_ledger", "kvq_seq_state", "kvq_export_unit",
@@ -528,13 +530,23 @@ class KVQCache:
 
     def append_kept(self, kept, seq_begin=0):
         """Append what evict kept: its sequence i to sequence seq_begin + i.
-        Lengths are checked for all of them before the first is appended."""
+        Lengths, and a paged cache's blocks, are checked for all of them before
+        the first is appended: all or none."""
         assert 0 <= seq_begin and seq_begin + len(kept.counts) <= self.cfg.batch, \
             f"{len(kept.counts)} sequences from {seq_begin} on do not fit a batch of {self.cfg.batch}"
+        blocks = 0  # that the appends will take from the pool
         for i, n in enumerate(kept.counts):
-            held = self.seq_state(seq_begin + i)["total"]
-            if held + n > self.capacity[seq_begin + i]:
-                raise KVQError(KVQ_ECAPACITY, f"sequence {seq_begin + i}: {held} + {n} tokens exceed its capacity")
+            seq, state = seq_begin + i, self.seq_state(seq_begin + i)
+            if state["total"] + n > self.capacity[seq]:
+                raise KVQError(KVQ_ECAPACITY, f"sequence {seq}: {state['total']} + {n} tokens exceed its capacity")
+            if n and self.pool_blocks:
+                flushed = max(0, state["window"] + n - self.cfg.residual_len) // self.cfg.group
+                if flushed > MAX_FLUSHED_GROUPS:
+                    raise KVQError(KVQ_EUNSUPPORTED, f"sequence {seq} would flush {flushed} groups in one append; a "
+                                                     f"paged cache takes at most {MAX_FLUSHED_GROUPS}")
+                blocks += flushed
+        if blocks and blocks > self.pool_state()[0]:
+            raise KVQError(KVQ_ECAPACITY, f"the appends need {blocks} new blocks; the pool has {self.pool_state()[0]} free")
         for i, n in enumerate(kept.counts):
             if n:
                 k, v, _ = kept.sequence(i)
