@@ -342,9 +342,11 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_con
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * ty + i, t = r / p.g, pos = t0 + t;
       if (t < tile_tok && pos < sq.len) {
-        // lse in the scores' units as a float and the factor that makes up for its rounding
+        // lse in the scores' units as a float and the factor that makes up for its
+        // rounding (from 2^24 on a weight is 0 or infinite with or without it, and an infinity has none)
         const float e = p.lse[(int64_t)(h * p.g + r - t * p.g) * p.n_tokens + sq.start + pos];
-        const float lse2 = __fmul_rn(e, p.lse_hi), f = exp2f(-(fmaf(e, p.lse_hi, -lse2) + e * p.lse_lo));
+        const float lse2 = __fmul_rn(e, p.lse_hi);
+        const float f = fabsf(lse2) < 0x1p24f ? exp2f(-(fmaf(e, p.lse_hi, -lse2) + e * p.lse_lo)) : 1.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (k0 + tx + 16 * j <= pos) sum[j] = fmaf(exp2f(fmaf(s[i][j], p.scale2, -lse2)), f, sum[j]);

@@ -193,9 +193,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (then >= 0) fetch_lse(then);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // -L = -lse * lse_hi - lse * lse_lo, cut into four pieces of 8 bits
-          const float hi = __fmul_rn(-now[e], p.lse_hi), rest = fmaf(-now[e], p.lse_hi, -hi) - now[e] * p.lse_lo;
-          const float b0 = __bfloat162float(__float2bfloat16_rn(hi)), left = hi - b0;
+          // -L = -lse * lse_hi - lse * lse_lo, cut into four pieces of 8 bits; an infinity is one piece
+          const float hi = __fmul_rn(-now[e], p.lse_hi), b0 = __bfloat162float(__float2bfloat16_rn(hi));
+          const bool whole = !(fabsf(b0) < INFINITY);
+          const float rest = whole ? 0.f : fmaf(-now[e], p.lse_hi, -hi) - now[e] * p.lse_lo;
+          const float left = whole ? 0.f : hi - b0;
           const float b1 = __bfloat162float(__float2bfloat16_rn(left)), last = left - b1 + rest;
           const float b2 = __bfloat162float(__float2bfloat16_rn(last));
           *reinterpret_cast<uint4*>(smem + L::kL + s * 2048 + (32 * e + lane) * 16) =
