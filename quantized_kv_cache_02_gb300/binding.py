@@ -452,7 +452,8 @@ def evict(k, v, weights, seq_lens, keep, first=0, recent=0):
     counts = [min(int(keep), int(n)) for n in seq_lens] if isinstance(keep, numbers.Integral) else [int(n) for n in keep]
     assert len(counts) == len(seq_lens), f"expected {len(seq_lens)} counts in keep, got {len(counts)}"
     torch, device = p.torch, k.device
-    rows = max(0, sum(counts)) * p.heads
+    # (counts past a sequence's length are refused by the call, not tried on the allocator)
+    rows = sum(max(0, min(n, int(most))) for n, most in zip(counts, seq_lens)) * p.heads
     k_out = torch.empty((rows, p.dim), dtype=k.dtype, device=device)
     v_out = torch.empty_like(k_out)
     index = torch.empty(rows, dtype=torch.int32, device=device)
