@@ -17,3 +17,27 @@ def test_counts_past_the_lengths_are_refused(torch, kvq):  # noqa: F811
             kvq.evict(k, v, w, [40, 20], keep)
         assert e.value.status == kvq.binding.KVQ_EINVAL
     assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "bfloat16"), (48, "bfloat16"), (64, "float32")])
+def test_strides_of_dimensions_of_one_entry_are_not_used(torch, kvq, d, dtype):  # noqa: F811
+    q, k, v = inputs(torch, 1, 1, 1, d, dtype, 23)
+    want, lse = kvq.prompt_attention(q, k, v, [1])
+    odd = [t.as_strided((1, 1, d), s) for t, s in zip((q, k, v), ((3, 7, 1), (0, 0, 1), (1 << 40, 5, 1)))]
+    out = torch.empty_like(q).as_strided((1, 1, d), (0, 1, 1))
+    _, l2 = kvq.prompt_attention(*odd, [1], out=out)
+    assert torch.equal(out.reshape(-1), v.reshape(-1)) and torch.equal(want.reshape(-1), v.reshape(-1))
+    assert torch.equal(lse, l2)
+    w = kvq.prompt_weights(odd[0], odd[1], lse, [1], 1)
+    assert torch.equal(w, kvq.prompt_weights(q, k, lse, [1], 1))
+    kept = kvq.evict(odd[1], odd[2], w, [1], 1)
+    assert torch.equal(kept.k, k[:, 0]) and torch.equal(kept.v, v[:, 0])
+    # one KV head of several tokens, one token of several heads
+    q, k, v = inputs(torch, 70, 4, 1, d, dtype, 24)
+    want, lse = kvq.prompt_attention(q, k, v, [70])
+    one = [t.as_strided((70, 1, d), (d, s, 1)) for t, s in ((k, 3), (v, 0))]
+    assert torch.equal(kvq.prompt_attention(q, *one, [70])[0], want)
+    assert torch.equal(kvq.prompt_weights(q, one[0], lse, [70], 9), kvq.prompt_weights(q, k, lse, [70], 9))
+    q, k, v = inputs(torch, 1, 4, 2, d, dtype, 25)
+    one = [t.as_strided((1, t.shape[1], d), (s, d, 1)) for t, s in ((q, 9), (k, 0), (v, 1))]
+    assert torch.equal(kvq.prompt_attention(*one, [1])[0], kvq.prompt_attention(q, k, v, [1])[0])
