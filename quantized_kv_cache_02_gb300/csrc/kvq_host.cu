@@ -86,6 +86,7 @@ kvq_status fail(kvq_status st, const char* fmt, ...) {
 }
 
 kvq_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();  // reported here: the thread's next CUDA call, of whoever's, does not report it again
   return fail(KVQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
