@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import numbers
 import os
+from operator import index
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvq.so")
@@ -297,7 +298,7 @@ def kvq_prompt_weights(prompt: kvq_prompt, q_ptr, k_ptr, lse_ptr, last, weights_
 
 def kvq_evict(prompt: kvq_prompt, k_ptr, v_ptr, weights_ptr, keep, first, recent, k_out_ptr, v_out_ptr, index_ptr,
               stream) -> None:
-    _check(load_library().kvq_evict(ctypes.byref(prompt), k_ptr, v_ptr, weights_ptr, _i64_array(keep), first, recent,
+    _check(load_library().kvq_evict(ctypes.byref(prompt), k_ptr, v_ptr, weights_ptr, _counts(keep), first, recent,
                                     k_out_ptr, v_out_ptr, index_ptr, stream))
 
 
@@ -329,8 +330,8 @@ def prompt_status(device=None) -> int:
 def _counts(values):
     try:
         return (ctypes.c_int64 * len(values))(*values)
-    except TypeError:  # integers of other kinds (numpy, tensors)
-        return _i64_array(values)
+    except TypeError:  # integers of other kinds (numpy, tensors); a fraction is no count
+        return (ctypes.c_int64 * len(values))(*[index(v) for v in values])
 
 
 class _Prompt:
@@ -418,7 +419,7 @@ def prompt_weights(q, k, lse, seq_lens, last, out=None):
     p.queries(q)
     p.rows("lse", lse, q.shape[1])
     out = p.rows("out", out, p.heads)
-    p.call(load_library().kvq_prompt_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(), int(last), out.data_ptr())
+    p.call(load_library().kvq_prompt_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(), index(last), out.data_ptr())
     return out
 
 
@@ -449,18 +450,21 @@ def evict(k, v, weights, seq_lens, keep, first=0, recent=0):
     p = _Prompt(k, seq_lens)
     p.values(v)
     p.rows("weights", weights, p.heads)
-    counts = [min(int(keep), int(n)) for n in seq_lens] if isinstance(keep, numbers.Integral) else [int(n) for n in keep]
+    if isinstance(keep, numbers.Integral):
+        counts = [min(index(keep), index(n)) for n in seq_lens]
+    else:
+        counts = [index(n) for n in keep]
     assert len(counts) == len(seq_lens), f"expected {len(seq_lens)} counts in keep, got {len(counts)}"
     torch, device = p.torch, k.device
     # (counts past a sequence's length are refused by the call, not tried on the allocator)
-    rows = sum(max(0, min(n, int(most))) for n, most in zip(counts, seq_lens)) * p.heads
+    rows = sum(max(0, min(n, index(most))) for n, most in zip(counts, seq_lens)) * p.heads
     k_out = torch.empty((rows, p.dim), dtype=k.dtype, device=device)
     v_out = torch.empty_like(k_out)
-    index = torch.empty(rows, dtype=torch.int32, device=device)
+    at = torch.empty(rows, dtype=torch.int32, device=device)
     p.call(load_library().kvq_evict, k.data_ptr(), v.data_ptr(), weights.data_ptr(),
-           _counts(counts), int(first), int(recent), k_out.data_ptr(), v_out.data_ptr(),
-           index.data_ptr())
-    return Kept(k_out, v_out, index, counts, p.heads)
+           _counts(counts), index(first), index(recent), k_out.data_ptr(), v_out.data_ptr(),
+           at.data_ptr())
+    return Kept(k_out, v_out, at, counts, p.heads)
 
 
 def kvq_kernel_launches() -> int:

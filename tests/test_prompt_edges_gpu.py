@@ -41,3 +41,14 @@ def test_strides_of_dimensions_of_one_entry_are_not_used(torch, kvq, d, dtype): 
     q, k, v = inputs(torch, 1, 4, 2, d, dtype, 25)
     one = [t.as_strided((1, t.shape[1], d), (s, d, 1)) for t, s in ((q, 9), (k, 0), (v, 1))]
     assert torch.equal(kvq.prompt_attention(*one, [1])[0], kvq.prompt_attention(q, k, v, [1])[0])
+
+
+def test_fractions_are_no_counts(torch, kvq):  # noqa: F811
+    q, k, v = inputs(torch, 40, 2, 2, 64, "bfloat16", 26)
+    lse = torch.zeros(2, 40, device="cuda")
+    w = torch.rand(2, 40, device="cuda")
+    for bad in (lambda: kvq.prompt_attention(q, k, v, [39.5]), lambda: kvq.prompt_weights(q, k, lse, [40], 3.5),
+                lambda: kvq.evict(k, v, w, [20, 20], [0.5, 0.5]), lambda: kvq.evict(k, v, w, [40], 0.5),
+                lambda: kvq.evict(k, v, w, [40], 10, first=0.5), lambda: kvq.evict(k, v, w, [40], 10, recent=1.5)):
+        with pytest.raises(TypeError):
+            bad()
