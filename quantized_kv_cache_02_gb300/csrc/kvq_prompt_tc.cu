@@ -247,10 +247,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     } else {
       // ============ MMAs, all issued by one lane ======================================
-      // The MMAs run in the order of issue.  With P over S, Q K^T of the next
-      // block may therefore overwrite P right behind the P V that reads it, and
-      // the arrival for S_j also says that the P V of block j - 1 is done.  With P
-      // apart, O's barrier says so, once a block.
+      // With P over S, Q K^T of the next block overwrites P right behind the P V
+      // that reads it.  They have different accumulators, for which the instruction
+      // set promises no order by itself: a tcgen05.fence between them, which orders
+      // the asynchronous tcgen05 instructions before it ahead of those behind it.
+      // The arrival for S_j then also says that the P V of block j - 1 is done.  With
+      // P apart, O's barrier says so, once a block.  (For 4096 tokens the fence takes
+      // nothing, a wait for the P V's completion 9 us of 104, and one S that the tiles
+      // share beside two P 14 us of 110.)
       constexpr uint32_t idesc_s = bf16_idesc(kRows, kKeys, false), idesc_o = bf16_idesc(kRows, D, true);
       const bool one = elect_one();
       auto scores = [&](int i, uint32_t kaddr) {
@@ -306,7 +310,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (one && (L::kApart || j + 1 == ni)) mma_commit(bar_o + 8 * i);
           // the next pair's wait passes while MMAs are queued
           if (i == (n1 > 0) && j + 1 < nmax) ok = landed(j + 1);
-          if (!L::kApart && j + 1 < ni) scores(i, kaddr);
+          if (!L::kApart && j + 1 < ni) {
+            tm_fence_before();
+            scores(i, kaddr);
+          }
         }
         if (ok && one) mma_commit(bar_empty + 8 * s);
       }
