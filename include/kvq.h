@@ -448,7 +448,9 @@ kvq_status kvq_compare(const void* key, const void* value, int64_t batch, int32_
  * softmax weights are rounded to bf16 before they meet v.  Nothing of another
  * sequence or of a later token reaches a result, infinities and NaN included;
  * an infinite or NaN element of v makes that element of the tokens from its own
- * on infinite or NaN.  Finite Values are to be small enough for fp32 sums of 2^8
+ * on infinite or NaN.  A row with a score of plus infinity or NaN has NaN in out
+ * and lse; a score of minus infinity weighs nothing, and a row of only such has
+ * NaN in out.  Finite Values are to be small enough for fp32 sums of 2^8
  * times their size.  out must not overlap the inputs, nor
  * its rows each other.  No gradient: like the rest of the library this serves
  * inference.  Only enqueues work on ``stream``; needs no workspace, and
@@ -463,7 +465,8 @@ kvq_status kvq_prompt_attention(const kvq_prompt* prompt, const void* q, const v
  *   weights[hkv][j] = sum over the g query heads h of hkv, over the counted
  *   tokens i >= j, of exp(q[i][h] . k[j][hkv] / sqrt(d) - lse[h][i]),
  * with lse as kvq_prompt_attention wrote it for the same prompt (entries of
- * queries that do not count are not read).  weights: float
+ * queries that do not count are not read; an infinite lse gives 0 or infinity as
+ * the formula does).  weights: float
  * [n_kv_heads][n_tokens], every token of every sequence written.  Summed in
  * fp32 in a fixed order: the same call gives the same bits.  The strides of v
  * and out are not used.  Errors as kvq_prompt_attention; last >= 1. */

@@ -321,7 +321,9 @@ def _status_word(device_index):
 
 def prompt_status(device=None) -> int:
     """The prompt kernels' status word on a device (synchronizes): 0 unless a
-    bounded wait gave up there since the process started."""
+    bounded wait gave up there since the process started, which leaves that
+    call's results undefined.  No call looks at it by itself.  Kernels captured
+    before any eager call on the device report nowhere."""
     import torch
     with torch.cuda.device(device):
         return int(_status_word(torch.cuda.current_device()).item())
@@ -397,7 +399,7 @@ def prompt_attention(q, k, v, seq_lens, out=None, lse=None):
     """Causal attention over packed prompts: q [tokens, n_q_heads, head_dim],
     k, v [tokens, n_kv_heads, head_dim] (bf16 or fp32; any strides of whole
     16-byte steps), seq_lens the sequences' lengths in order.  Returns (out,
-    lse): out like q, lse float32 [n_q_heads, tokens]."""
+    lse): out like q, lse float32 [n_q_heads, tokens].  No gradient."""
     p = _Prompt(k, seq_lens)
     p.queries(q)
     p.values(v)

@@ -183,6 +183,13 @@ int64_t fill_tiles(const std::vector<kvq::PromptSeq>& seqs, int hkv, int step, k
 // half a step of each partial sum on average, and a step is 2^-23 / (2 ln 2) of
 // its number on average.  The relative loss of a score whose partial sums add up to
 // ``sums`` times its size, by which its factor is raised.
+// An estimate, for channels whose products are spread in size and sign.  Measured
+// on normal queries and Keys (1024 tokens, d = 128, all weights' sum off by; without
+// the factor in brackets): plain 0.5e-7 (1.3e-7), a heavy channel in every 16 0.8e-7
+// (10e-7), the heavy ones all first 0.8e-7 (5.8e-7), all last 1.6e-7 (3.4e-7).
+// Where nothing is rounded off (products of one sign, close in size) the factor
+// itself is left over, 0.9e-7 of the score; where small products of one sign follow
+// one heavy step, each loses its own low bits, and 5e-7 of the score stay lost.
 double rounding_loss(double sums) { return 0.5 * sums * std::ldexp(1.0, -23) / (2.0 * std::log(2.0)); }
 
 // sqrt(d) for the scores: their factor, and lse in their units -- on the tensor

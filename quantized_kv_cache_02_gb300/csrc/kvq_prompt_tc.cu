@@ -24,11 +24,21 @@
 // the power limit).  At d = 64 the softmax: 256 exponentials a scheduler for a
 // block, measured some 2400 cycles with the maxima, sums and conversions.  Tried:
 // the block's maximum beside the first half's exponentials (105 us for 4096
-// tokens), half a row a thread on sixteen warps (113 us), a MMA warp a tile (116
-// us: the tiles fall into step).
-// The running maximum moves only when a score passes it by 2^8 (a row's sums
-// stay exact in fp32 either way), so O is rescaled rarely and by the softmax
-// threads themselves.
+// tokens), half a row a thread on sixteen warps (113 us; at d = 64 30 us where 27
+// are taken), a MMA warp a tile (116 us: the tiles fall into step).
+//
+// P is rounded to bf16 because V is bf16 and an MMA takes operands of one type: a
+// second MMA on what the rounding leaves would double the P V.  It is off by at
+// most 2^-8 of each weight, as the output's own rounding is of the output: against
+// 64 bits the output is off by 2.1e-3 where fp32 weights leave 1.7e-3 (4096
+// tokens).  The sum l, and lse with it, takes the weights before that rounding.
+//
+// One pass with a running maximum and sum is Milakov and Gimelshein's ("Online
+// normalizer calculation for softmax", 2018).  Here the maximum moves only when a
+// score passes it by 2^8, a published refinement, so O is rescaled rarely and by
+// the softmax threads themselves.  A maximum that lags scales all terms of a row by
+// one factor of at most 2^8: the relative roundings stay as they are, and 8 bits of
+// the exponent's range go (kvq.h on the size of Values).
 // ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d) + M) V.)
 
 #include <cfloat>

@@ -52,3 +52,25 @@ def test_fractions_are_no_counts(torch, kvq):  # noqa: F811
                 lambda: kvq.evict(k, v, w, [40], 10, first=0.5), lambda: kvq.evict(k, v, w, [40], 10, recent=1.5)):
         with pytest.raises(TypeError):
             bad()
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bfloat16"), (64, "bfloat16"), (96, "bfloat16"), (128, "float32")])
+def test_infinite_scores(torch, kvq, d, dtype):  # noqa: F811
+    """Plus infinity makes out and lse of its rows NaN and reaches no other; rows of minus infinity alone
+    have an lse of minus infinity."""
+    n, hq, hkv = 400, 4, 2
+    q, k, v = inputs(torch, n, hq, hkv, d, dtype, 27)
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    want, lse = kvq.prompt_attention(q, k, v, [n])
+    high = k.clone()
+    high[333, 1, 0] = torch.inf
+    got, l2 = kvq.prompt_attention(q, high, v, [n])
+    assert got[333:, 2:].isnan().all() and l2[2:, 333:].isnan().all()
+    got[333:, 2:], l2[2:, 333:] = want[333:, 2:], lse[2:, 333:]
+    assert torch.equal(got, want) and torch.equal(l2, lse)
+    low = k.clone()
+    low[:140, 0, 0] = -torch.inf
+    got, l2 = kvq.prompt_attention(q, low, v, [n])
+    assert got[:140, :2].isnan().all() and l2[:2, :140].isneginf().all()
+    assert got[140:].isfinite().all() and l2[:2, 140:].isfinite().all()
+    assert torch.equal(got[:, 2:], want[:, 2:]) and torch.equal(l2[2:], lse[2:])
