@@ -233,7 +233,8 @@ cudaError_t launch_restore(const RestoreParams& p, cudaStream_t s) {
   const size_t smem = 2 * (size_t)p.geom.page_bytes +
                       ((size_t)p.G * p.D + (size_t)nm * (p.D + p.G)) * sizeof(float);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(restore_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // all there is, not this cache's need: the limit is a state of the kernel that all caches and threads share
+    const cudaError_t e = cudaFuncSetAttribute(restore_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
   }
   RestoreParams q = p;

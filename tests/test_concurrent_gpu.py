@@ -19,6 +19,12 @@ int weights_calls(kvq_status (*fn)(const kvq_prompt*, const void*, const void*, 
   for (int i = 0; i < n; ++i) failed += fn(p, q, k, lse, 32, w, stream) != KVQ_OK;
   return failed;
 }
+int restore_calls(kvq_status (*fn)(const kvq_cache*, int32_t, int32_t, void*, void*, int64_t, kvq_dtype, void*),
+                  const kvq_cache* c, void* k, void* v, int64_t t_stride, void* stream, int n) {
+  int failed = 0;
+  for (int i = 0; i < n; ++i) failed += fn(c, 0, 1, k, v, t_stride, KVQ_BF16, stream) != KVQ_OK;
+  return failed;
+}
 """
 
 
@@ -48,7 +54,7 @@ def calls(tmp_path_factory):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([cc, "-O2", "-shared", "-fPIC", "-I", os.path.join(root, "include"), str(at / "calls.c"), "-o",
                     str(at / "calls.so")], check=True)
-    return ctypes.CDLL(str(at / "calls.so")).weights_calls
+    return ctypes.CDLL(str(at / "calls.so"))
 
 
 def test_weights_of_several_head_dims(torch, kvq, calls):
@@ -58,8 +64,8 @@ def test_weights_of_several_head_dims(torch, kvq, calls):
 
     def run(p, q, k, lse, out, stream):
         gate.wait()
-        failed.append(calls(kvq.load_library().kvq_prompt_weights, ctypes.byref(p.c), *(ctypes.c_void_p(x.data_ptr())
-                            for x in (q, k, lse, out)), ctypes.c_void_p(stream.cuda_stream), 20000))
+        failed.append(calls.weights_calls(kvq.load_library().kvq_prompt_weights, ctypes.byref(p.c), *(ctypes.c_void_p(x.data_ptr())
+                                          for x in (q, k, lse, out)), ctypes.c_void_p(stream.cuda_stream), 20000))
 
     for d in (256, 16, 256, 64):
         q = torch.randn(sum(lens), 4, d, device="cuda")
@@ -92,3 +98,32 @@ def test_a_second_cache_leaves_the_first_ones_appends_alone(torch, kvq, dtype):
     torch.cuda.synchronize()
     a, b = big.export_unit(0, 1), alone.export_unit(0, 1)
     assert big.seq_state(0) == alone.seq_state(0) and all((a[x] == b[x]).all() for x in a)
+
+
+def test_restores_of_two_caches(torch, kvq, calls):
+    """A restore's shared memory goes by its cache's group."""
+    threads, results, failed = [], [], []
+    gate = threading.Barrier(4)
+
+    def run(cache, k, v, stream):
+        gate.wait()
+        failed.append(calls.restore_calls(kvq.load_library().kvq_restore, ctypes.c_void_p(cache.handle),
+                                          ctypes.c_void_p(k.data_ptr()), ctypes.c_void_p(v.data_ptr()),
+                                          ctypes.c_int64(k.shape[2]), ctypes.c_void_p(stream.cuda_stream), 20000))
+
+    for group in (128, 64, 128, 64):
+        cache = kvq.KVQCache(1, 2, 4, 128, 64, group, 7, 512)
+        cache.append(*(torch.randn(1, 2, 400, 128, device="cuda").bfloat16() for _ in range(2)))
+        want = cache.restore()
+        got = [torch.empty_like(t) for t in want]
+        results.append((cache, want, got))
+        threads.append(threading.Thread(target=run, args=(cache, *got, torch.cuda.Stream())))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0, 0, 0]
+    for _, want, got in results:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
