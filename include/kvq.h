@@ -190,6 +190,54 @@ typedef struct kvq_prompt {
                            undefined); never cleared by the library */
 } kvq_prompt;
 
+/* Queries and the states they attend to (kvq_cross_attention).  Queries are
+ * packed: sequence i takes the q_lens[i] rows of q and out after those of the
+ * sequences before it.  Its states are the kv_lens[i] rows of k and v from row
+ * kv_starts[i] on; with kv_starts NULL they are packed like the queries.  Starts may
+ * be in any order and states may be shared, so padded batches and several
+ * sequences over one encoding are taken as they are.  Lengths may be 0.  Rows
+ * outside the sequences are neither read into a result nor written.  Strides as
+ * in kvq_prompt. */
+typedef struct kvq_cross {
+  int32_t n_seqs;       /* >= 1 */
+  int32_t n_q_heads;    /* Hq, a multiple of Hkv with g = Hq / Hkv <= 8 */
+  int32_t n_kv_heads;   /* Hkv >= 1 */
+  int32_t head_dim;     /* d: a multiple of 16, 16 <= d <= 256 */
+  int32_t dtype;        /* kvq_dtype of q, k, v and out */
+  const int64_t* q_lens;    /* host arrays of n_seqs entries, read during the call */
+  const int64_t* kv_lens;
+  const int64_t* kv_starts; /* or NULL */
+  int64_t n_q_tokens;   /* rows of q and out (>= the q_lens' sum, <= 2^30) */
+  int64_t n_kv_tokens;  /* rows of k and v (<= 2^30) */
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int32_t* status;      /* device word or NULL, as in kvq_prompt */
+} kvq_cross;
+
+/* How rotary positions turn a head (kvq_rotary): pair i of its channels is turned
+ * by position[axis[i]] * frequency[i] radians; a token has n_axes positions
+ * (time, height and width of a video, say).  Channels past 2 n_pairs stay as they are. */
+typedef struct kvq_rotary_plan {
+  int32_t head_dim;     /* d: a multiple of 16, 16 <= d <= 256 */
+  int32_t n_axes;       /* 1..4 */
+  int32_t n_pairs;      /* 1..d / 2 */
+  int32_t interleaved;  /* 0: pair i is channels i and i + n_pairs; else 2i and 2i + 1 */
+  const double* frequency; /* host arrays of n_pairs entries, read during the call; |f| <= 2^20 */
+  const int32_t* axis;     /* 0..n_axes - 1 */
+} kvq_rotary_plan;
+
+/* One tensor [n_tokens][n_heads][head_dim] to turn, and where to.  Strides in
+ * elements as in kvq_prompt; out may be input, with the same strides. */
+typedef struct kvq_rotary_tensor {
+  const void* input;
+  void* out;
+  int64_t in_token_stride, in_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int32_t n_heads;      /* 1..65535 */
+} kvq_rotary_tensor;
+
 typedef struct kvq_cache kvq_cache; /* opaque host handle */
 
 /*
@@ -283,6 +331,24 @@ kvq_status kvq_create_segmented(const kvq_config* cfg, const int64_t* capacity_p
  * reuse the blocks, so issue everything on one stream (or order the streams)
  * around a release.  KVQ_EINVAL for a bad range. */
 kvq_status kvq_release(kvq_cache* cache, int32_t seq_begin, int32_t n_seqs);
+
+/* Copy whole sequences: for each i < n, all at once, sequence dst[i] becomes what
+ * src[i] held before the call (counters, codes, scales and window, bit for bit) and
+ * what it held itself is released.  One prompt sampled several times, a beam
+ * search's survivors over the beams that it drops, beams that change places: src may
+ * repeat and may be a dst as well; dst may not repeat; src[i] == dst[i] is no
+ * work.  src, dst: host arrays.  A paged cache's blocks are shared, not copied: a
+ * flushed page is never written again, a block returns to the pool when the last
+ * sequence that holds it lets go (kvq_release, or a fork over it), and kvq_bytes
+ * counts it for each.  The pool needs no free blocks.  A contiguous or
+ * segmented cache's codes and scales are copied.  Windows are copied in every cache.
+ * Only enqueues work on ``stream`` (the counters change in the call: a replayed graph
+ * repeats the copies alone); the order around it is the caller's, as for
+ * kvq_release.  Errors before any launch, the state unchanged: KVQ_EINVAL (bad
+ * index, a dst twice), KVQ_ECAPACITY (src[i] holds more tokens than dst[i] may),
+ * KVQ_EUNSUPPORTED (more than 512 sequences that depend on one another: copies of
+ * one source, or a chain of sources that are written too). */
+kvq_status kvq_fork(kvq_cache* cache, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
 
 /* Free and total blocks of a paged cache's pool (both 0 for a contiguous
  * cache).  Host counters, no device access. */
@@ -488,6 +554,42 @@ kvq_status kvq_prompt_weights(const kvq_prompt* prompt, const void* q, const voi
  * as kvq_prompt_attention. */
 kvq_status kvq_evict(const kvq_prompt* prompt, const void* k, const void* v, const float* weights, const int64_t* keep,
                      int64_t first, int64_t recent, void* k_out, void* v_out, int32_t* index, void* stream);
+
+/* Attention over other states than the queries' own ("KV Cache 与自回归视频生成",
+ * softmax(Q K^T / sqrt(d)) V without a mask, with attn_step's head mapping): an
+ * encoder's states, a text prompt's beside a video's frames.  For token i of each
+ * sequence and query head h, over the sequence's states j,
+ *   out[i][h] = sum_j softmax_j(q[i][h] . k[j][h / g] / sqrt(d)) v[j][h / g],
+ *   lse[h][i] = log sum_j exp(q[i][h] . k[j][h / g] / sqrt(d)).
+ * q, out: [n_q_tokens][n_q_heads][head_dim]; k, v: [n_kv_tokens][n_kv_heads]
+ * [head_dim]; lse: float [n_q_heads][n_q_tokens] (natural logarithm; may be
+ * NULL).  Without states out is 0 and lse minus infinity.  One new token a sequence
+ * is the call with q_lens of 1: sequences of few queries have their states split
+ * among CTAs that join their results.  Roundings, infinities, NaN, gradients,
+ * streams and errors as kvq_prompt_attention.  Summed in a fixed order: the same
+ * call gives the same bits. */
+kvq_status kvq_cross_attention(const kvq_cross* cross, const void* q, const void* k, const void* v, void* out,
+                               float* lse, void* stream);
+
+/* Rotary positions ("KV Cache 与自回归视频生成": Keys enter the cache after
+ * them).  Every head of n_tensors tensors (q, or q and k; 1 or 2) of ``dtype`` is
+ * turned by the plan:
+ *   out[x] = input[x] cos t - input[y] sin t,  out[y] = input[x] sin t + input[y] cos t
+ * for pair (x, y) and t = positions[token][axis] * frequency; by -t with inverse
+ * != 0, which undoes it and takes gradients of out to gradients of input.
+ * positions: device integers of position_bytes (4 or 8) bytes, element (token, axis)
+ * at token * position_token_stride + axis * position_axis_stride; any value, negative
+ * ones too.  Angles come from integer arithmetic modulo whole turns: those of far
+ * positions are as good as those of near ones (within 2^-32 of a turn for positions
+ * up to 2^32, beside the frequency's own rounding to 2^-53 of itself).  Products
+ * and sums are fp32, rounded once to dtype.  Channels past the pairs are copied.
+ * Only enqueues work on ``stream``; no workspace.  An out that is not its own input
+ * must not overlap any input, nor the other out.  Errors before any launch: KVQ_EINVAL
+ * (plan, shape, stride, NULL or misaligned pointer, memory that is not on the current
+ * device), KVQ_EUNSUPPORTED (head_dim, strides of 2^40 bytes, size). */
+kvq_status kvq_rotary(const kvq_rotary_plan* plan, const void* positions, int32_t position_bytes,
+                      int64_t position_token_stride, int64_t position_axis_stride, int64_t n_tokens, int32_t dtype,
+                      const kvq_rotary_tensor* tensors, int32_t n_tensors, int32_t inverse, void* stream);
 
 /* Size in bytes of one group page for this configuration (0 if invalid). */
 size_t kvq_page_bytes(const kvq_config* cfg);

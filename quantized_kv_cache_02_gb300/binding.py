@@ -29,7 +29,7 @@ EXPORTED = ("kvq_required_bytes", "kvq_create", "kvq_append", "kvq_decode_attent
             "kvq_last_error", "kvq_decode_attention_noalloc", "kvq_restore", "kvq_dense_decode_attention",
             "kvq_compare", "kvq_required_bytes_paged", "kvq_create_paged", "kvq_release", "kvq_pool_state",
             "kvq_required_bytes_segmented", "kvq_create_segmented", "kvq_decode_step",
-            "kvq_prompt_attention", "kvq_prompt_weights", "kvq_evict")
+            "kvq_prompt_attention", "kvq_prompt_weights", "kvq_evict", "kvq_cross_attention", "kvq_rotary", "kvq_fork")
 
 
 class kvq_config(ctypes.Structure):
@@ -70,6 +70,25 @@ class kvq_prompt(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("n_tokens", "q_token_stride", "q_head_stride", "k_token_stride",
                                       "k_head_stride", "v_token_stride", "v_head_stride", "out_token_stride",
                                       "out_head_stride")] + [("status", ctypes.c_void_p)]
+
+
+class kvq_cross(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_q_heads", "n_kv_heads", "head_dim", "dtype")] + [
+        (n, ctypes.POINTER(ctypes.c_int64)) for n in ("q_lens", "kv_lens", "kv_starts")] + [
+        (n, ctypes.c_int64) for n in ("n_q_tokens", "n_kv_tokens", "q_token_stride", "q_head_stride", "k_token_stride",
+                                      "k_head_stride", "v_token_stride", "v_head_stride", "out_token_stride",
+                                      "out_head_stride")] + [("status", ctypes.c_void_p)]
+
+
+class kvq_rotary_plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "n_axes", "n_pairs", "interleaved")] + [
+        ("frequency", ctypes.POINTER(ctypes.c_double)), ("axis", ctypes.POINTER(ctypes.c_int32))]
+
+
+class kvq_rotary_tensor(ctypes.Structure):
+    _fields_ = [("input", ctypes.c_void_p), ("out", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("in_token_stride", "in_head_stride", "out_token_stride", "out_head_stride")] + [
+        ("n_heads", ctypes.c_int32)]
 
 
 class KVQError(RuntimeError):
@@ -119,6 +138,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvq_prompt_attention": ([P(kvq_prompt), V, V, V, V, V, V], ctypes.c_int),
         "kvq_prompt_weights": ([P(kvq_prompt), V, V, V, I64, V, V], ctypes.c_int),
         "kvq_evict": ([P(kvq_prompt), V, V, V, P(I64), I64, I64, V, V, V, V], ctypes.c_int),
+        "kvq_cross_attention": ([P(kvq_cross), V, V, V, V, V, V], ctypes.c_int),
+        "kvq_rotary": ([P(kvq_rotary_plan), V, I32, I64, I64, I64, I32, P(kvq_rotary_tensor), I32, I32, V],
+                       ctypes.c_int),
+        "kvq_fork": ([V, P(I32), P(I32), I32, V], ctypes.c_int),
         "kvq_destroy": ([V], None),
         "kvq_last_error": ([], ctypes.c_char_p),
     }
@@ -302,6 +325,22 @@ def kvq_evict(prompt: kvq_prompt, k_ptr, v_ptr, weights_ptr, keep, first, recent
                                     k_out_ptr, v_out_ptr, index_ptr, stream))
 
 
+def kvq_cross_attention(cross: kvq_cross, q_ptr, k_ptr, v_ptr, out_ptr, lse_ptr, stream) -> None:
+    _check(load_library().kvq_cross_attention(ctypes.byref(cross), q_ptr, k_ptr, v_ptr, out_ptr, lse_ptr, stream))
+
+
+def kvq_rotary(plan: kvq_rotary_plan, positions_ptr, position_bytes, position_token_stride, position_axis_stride,
+               n_tokens, dtype, tensors, n_tensors, inverse, stream) -> None:
+    _check(load_library().kvq_rotary(ctypes.byref(plan), positions_ptr, position_bytes, position_token_stride,
+                                     position_axis_stride, n_tokens, dtype, tensors, n_tensors, inverse, stream))
+
+
+def kvq_fork(handle, src, dst, stream) -> None:
+    assert len(src) == len(dst), f"{len(src)} sequences to copy to {len(dst)}"
+    pairs = [(ctypes.c_int32 * len(x))(*[index(i) for i in x]) for x in (src, dst)]
+    _check(load_library().kvq_fork(handle, *pairs, len(src), stream))
+
+
 # ---- prompt operators on torch tensors ---------------------------------------
 #
 # A short prompt's call is bound by the host (the kernels take 5 to 15 us), so
@@ -469,6 +508,135 @@ def evict(k, v, weights, seq_lens, keep, first=0, recent=0):
     return Kept(k_out, v_out, at, counts, p.heads)
 
 
+# ---- beside the cache: cross attention, rotary positions --------------------------
+
+def _call_on(torch, device, fn, *args):
+    """fn(*args, torch's current stream on device), with that device current."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _call_on(torch, device, fn, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status:
+        _check(status)
+
+
+def _rows_like(torch, name, t, like, heads, tokens, dim):
+    """Strides of a [tokens, heads, dim] tensor with like's dtype and device (heads None: any)."""
+    shape, stride = t.shape, t.stride()
+    assert len(shape) == 3 and shape[0] == tokens and shape[2] == dim and heads in (None, shape[1]), \
+        f"expected {name} of shape {(tokens, heads or 'heads', dim)}, got {tuple(shape)}"
+    assert t.dtype == like.dtype and t.get_device() == like.get_device(), f"{name} must match the dtype and device of q"
+    assert stride[2] == 1, f"{name}'s last dimension must be contiguous"
+    return stride[0], stride[1]
+
+
+def _dtype_of(torch, q):
+    assert q.is_cuda and q.dim() == 3, "q must be a CUDA tensor [tokens, heads, head_dim]"
+    assert q.dtype == torch.bfloat16 or q.dtype == torch.float32, f"expected bfloat16 or float32, got {q.dtype}"
+    return KVQ_BF16 if q.dtype == torch.bfloat16 else KVQ_FP32
+
+
+def cross_attention(q, k, v, q_lens, kv_lens, kv_starts=None, out=None, lse=None):
+    """Attention of packed queries q [tokens, n_q_heads, head_dim] over other
+    states k, v [rows, n_kv_heads, head_dim] (bf16 or fp32; any strides of
+    whole 16-byte steps).  Sequence i has q_lens[i] queries and the kv_lens[i]
+    rows of k and v from kv_starts[i] on (None: packed like the queries; starts
+    may repeat, so sequences can share states).  Returns (out, lse): out like q,
+    lse float32 [n_q_heads, tokens]; over no states 0 and minus infinity.
+    q_lens of 1 is the form for single tokens.  No gradient."""
+    import torch
+    dtype = _dtype_of(torch, q)
+    device, (tokens, heads, dim) = q.get_device(), q.shape
+    rows, kv_heads = k.shape[0], k.shape[1]
+    lens, states = _counts(q_lens), _counts(kv_lens)
+    assert len(states) == len(lens), f"expected {len(lens)} lengths in kv_lens, got {len(states)}"
+    c = kvq_cross(len(lens), heads, kv_heads, dim, dtype, lens, states)
+    if kv_starts is not None:
+        c.kv_starts = starts = _counts(kv_starts)
+        assert len(starts) == len(lens), f"expected {len(lens)} starts in kv_starts, got {len(starts)}"
+    c.n_q_tokens, c.n_kv_tokens = tokens, rows
+    c.q_token_stride, c.q_head_stride = _rows_like(torch, "q", q, q, heads, tokens, dim)
+    c.k_token_stride, c.k_head_stride = _rows_like(torch, "k", k, q, kv_heads, rows, dim)
+    c.v_token_stride, c.v_head_stride = _rows_like(torch, "v", v, q, kv_heads, rows, dim)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    c.out_token_stride, c.out_head_stride = _rows_like(torch, "out", out, q, heads, tokens, dim)
+    if lse is None:
+        lse = torch.empty((heads, tokens), dtype=torch.float32, device=q.device)
+    else:
+        assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.get_device() == device and \
+            lse.shape == (heads, tokens), f"lse must be a contiguous float32 tensor {(heads, tokens)} on q's device"
+    word = _prompt_status.get(device)
+    if word is None:
+        word = _status_word(device)
+    if word is not None:
+        c.status = word.data_ptr()
+    _call_on(torch, device, load_library().kvq_cross_attention, ctypes.byref(c), q.data_ptr(), k.data_ptr(),
+             v.data_ptr(), out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+class Rotary:
+    """How rotary positions turn a head: its pair i is turned by
+    position[axes[i]] * frequencies[i] radians.  Pairs are the halves of the first
+    2 * len(frequencies) channels, (i, i + n), or with interleaved neighbours,
+    (2i, 2i + 1); channels past them stay as they are.  axes None: one axis."""
+
+    def __init__(self, head_dim, frequencies, axes=None, interleaved=False):
+        frequencies = [float(f) for f in frequencies]
+        axes = [0] * len(frequencies) if axes is None else [index(a) for a in axes]
+        assert len(axes) == len(frequencies), f"expected {len(frequencies)} axes, got {len(axes)}"
+        assert axes and min(axes) >= 0, "at least one pair, and no negative axis"
+        self.head_dim, self.frequencies, self.axes, self.interleaved = index(head_dim), frequencies, axes, bool(interleaved)
+        self.n_axes = max(axes) + 1
+        self.c = kvq_rotary_plan(self.head_dim, self.n_axes, len(axes), self.interleaved,
+                                 (ctypes.c_double * len(axes))(*frequencies), (ctypes.c_int32 * len(axes))(*axes))
+
+    @classmethod
+    def sections(cls, head_dim, sections, theta=10000.0, restart=False, interleaved=False):
+        """Runs of sections[a] pairs for axis a.  One series of frequencies,
+        theta ** (-i / pairs), falls over all pairs, or with restart each
+        axis has its own, theta ** (-i / sections[a])."""
+        axes = [a for a, n in enumerate(sections) for _ in range(index(n))]
+        if restart:
+            freq = [theta ** (-i / n) for n in sections for i in range(n)]
+        else:
+            freq = [theta ** (-i / len(axes)) for i in range(len(axes))]
+        return cls(head_dim, freq, axes, interleaved)
+
+
+def rotary(q, k, positions, plan, q_out=None, k_out=None, inverse=False):
+    """Turn the heads of q [tokens, n_q_heads, head_dim] and k [tokens,
+    n_kv_heads, head_dim] (or None) to their positions (int32 or int64 [tokens,
+    n_axes], or [tokens] for one axis; any values) by a Rotary plan, in one launch.
+    Returns (q_out, k_out), made where None; q_out=q and k_out=k turn in place.
+    inverse turns back: it undoes the call, and takes gradients through it."""
+    import torch
+    dtype = _dtype_of(torch, q)
+    device, (tokens, heads, dim) = q.get_device(), q.shape
+    assert dim == plan.head_dim, f"q has heads of {dim} channels, the plan of {plan.head_dim}"
+    assert positions.dtype == torch.int64 or positions.dtype == torch.int32, \
+        f"positions must be int32 or int64, got {positions.dtype}"
+    assert positions.get_device() == device, "positions must be on q's device"
+    shape, stride = tuple(positions.shape), positions.stride()
+    assert shape == (tokens, plan.n_axes) or (shape == (tokens,) and plan.n_axes == 1), \
+        f"expected positions of shape {(tokens, plan.n_axes)}, got {shape}"
+    pairs = [(q, "q", q_out)] if k is None else [(q, "q", q_out), (k, "k", k_out)]
+    assert k is not None or k_out is None, "k_out without k"
+    tensors, results = (kvq_rotary_tensor * 2)(), []
+    for t, (x, name, y) in zip(tensors, pairs):
+        t.in_token_stride, t.in_head_stride = _rows_like(torch, name, x, q, None, tokens, dim)
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        t.out_token_stride, t.out_head_stride = _rows_like(torch, name + "_out", y, q, x.shape[1], tokens, dim)
+        t.input, t.out, t.n_heads = x.data_ptr(), y.data_ptr(), x.shape[1]
+        results.append(y)
+    _call_on(torch, device, load_library().kvq_rotary, ctypes.byref(plan.c), positions.data_ptr(),
+             8 if positions.dtype == torch.int64 else 4, stride[0], stride[1] if len(stride) > 1 else 0, tokens, dtype,
+             tensors, len(pairs), bool(inverse))
+    return (results[0], results[1]) if k is not None else (results[0], None)
+
+
 def kvq_kernel_launches() -> int:
     return load_library().kvq_kernel_launches()
 
@@ -622,6 +790,15 @@ class KVQCache:
 
     def release(self, seq_begin=0, n_seqs=1):
         kvq_release(self.handle, seq_begin, n_seqs)
+
+    def fork(self, src, dst):
+        """Sequence dst[i] becomes what src[i] held before the call, all at
+        once (ints, or sequences of ints; one src goes to every dst); what dst
+        held is released.  A paged cache's blocks are shared, not copied."""
+        src, dst = ([x] if isinstance(x, numbers.Integral) else x for x in (src, dst))
+        if len(src) == 1:
+            src = list(src) * len(dst)
+        kvq_fork(self.handle, src, dst, self._stream())
 
     def pool_state(self):
         """(free blocks, pool blocks) of a paged cache."""

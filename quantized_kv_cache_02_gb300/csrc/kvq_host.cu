@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <new>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -19,7 +20,7 @@
 #include <vector>
 
 #include "../../include/kvq.h"
-#include "kvq_host.h"
+#include "kvq_args.h"
 #include "kvq_internal.h"
 
 using kvq::SeqCounters;
@@ -43,6 +44,7 @@ struct kvq_cache {
   int32_t* table;                            // device [batch][table_stride]
   std::vector<int32_t> free_blocks;
   std::vector<std::vector<int32_t>> blocks;  // host copy of each sequence's table
+  std::vector<int32_t> block_users;          // sequences that hold each block (kvq_fork shares them)
   // segmented mode (the whole overflow of an append is one segment): token-major
   // codes and scales; cfg.group is 1 inside (a "page" is one token)
   bool segmented;
@@ -420,6 +422,7 @@ kvq_status create(const kvq_config* cfg, const int64_t* capacity_per_seq, int64_
   c->table_stride = a.table_stride;
   c->blocks.assign(cfg->batch, {});
   for (int64_t blk = pool_blocks - 1; blk >= 0; --blk) c->free_blocks.push_back((int32_t)blk);
+  c->block_users.assign((size_t)pool_blocks, 0);
   c->device = attr.device;
   int cur = 0;
   cudaGetDevice(&cur);
@@ -488,6 +491,15 @@ kvq_status create(const kvq_config* cfg, const int64_t* capacity_per_seq, int64_
   }
   *out = c;
   return KVQ_OK;
+}
+
+// Sequence b lets go of its blocks; those that no fork of it holds go back to the
+// pool, most recently taken first, so that a release followed by the same appends
+// hands the blocks out in the same order again.
+void drop_blocks(kvq_cache* c, int b) {
+  for (auto it = c->blocks[b].rbegin(); it != c->blocks[b].rend(); ++it)
+    if (--c->block_users[*it] == 0) c->free_blocks.push_back(*it);
+  c->blocks[b].clear();
 }
 
 // Append to a segmented cache: zero the segment maxima of the sequences, run
@@ -655,6 +667,7 @@ static kvq_status append_impl(kvq_cache* c, const void* new_k, const void* new_v
     for (int64_t k = 0; k < new_blocks; ++k) {
       taken.push_back(c->free_blocks.back());
       c->free_blocks.pop_back();
+      c->block_users[taken.back()] = 1;
     }
   }
   size_t next_taken = 0;
@@ -1143,14 +1156,195 @@ kvq_status kvq_release(kvq_cache* c, int32_t seq_begin, int32_t n_seqs) {
     return fail(KVQ_EINVAL, "sequence range [%d, %d) is outside [0, %d)", seq_begin, seq_begin + n_seqs,
                 c->cfg.batch);
   for (int b = seq_begin; b < seq_begin + n_seqs; ++b) {
-    // most recently taken first, so that a release followed by the same appends
-    // hands the blocks out in the same order again
-    for (auto it = c->blocks[b].rbegin(); it != c->blocks[b].rend(); ++it) c->free_blocks.push_back(*it);
-    c->blocks[b].clear();
+    drop_blocks(c, b);
     if (c->segmented) c->seg_starts[b].clear();
     c->total[b] = c->quantized[b] = c->last_flushed[b] = 0;
   }
   return KVQ_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The steps of pairs src[i] -> dst[i] (distinct dst, src[i] != dst[i]), a
+// component a vector.  Every sequence has at most one source, so a component is a
+// tree or one cycle with trees on it.  A sequence that is a source is read before
+// its own copy arrives: the trees from their leaves up, then the cycle against its
+// direction, one of its sequences held since the start.
+struct ForkPlan {
+  struct Step {
+    int32_t src;
+    bool held;
+    std::vector<int32_t> dst;  // empty: hold
+  };
+  std::vector<std::vector<Step>> components;
+};
+
+void plan_fork(int batch, const std::vector<int32_t>& from, ForkPlan* plan) {
+  // from[b]: the source of sequence b, or -1
+  std::vector<std::vector<int32_t>> copies(batch);
+  for (int b = 0; b < batch; ++b)
+    if (from[b] >= 0) copies[from[b]].push_back(b);
+  std::vector<char> seen(batch, 0);
+  std::vector<int32_t> walk(batch, -1);
+  for (int b = 0; b < batch; ++b) {
+    if (seen[b] || (from[b] < 0 && copies[b].empty())) continue;
+    // up to the root, or onto the cycle
+    int root = b;
+    while (from[root] >= 0 && walk[root] != b) {
+      walk[root] = b;
+      root = from[root];
+    }
+    const bool cycle = from[root] >= 0;
+    std::vector<int32_t> ring;  // the cycle: root, its source, that one's source ...
+    for (int x = root; cycle && (ring.empty() || x != root); x = from[x]) ring.push_back(x);
+    for (int32_t x : ring) seen[x] = 1;
+    // trees below the root (or the cycle), parents before children; run backwards below
+    std::vector<int32_t> start = cycle ? ring : std::vector<int32_t>{root};
+    for (size_t at = 0; at < start.size(); ++at) {
+      seen[start[at]] = 1;
+      for (int32_t x : copies[start[at]])
+        if (!seen[x]) start.push_back(x);
+    }
+    const size_t tops = cycle ? ring.size() : 0;
+    std::vector<ForkPlan::Step> steps;
+    if (cycle) steps.push_back({root, false, {}});
+    for (size_t at = start.size(); at-- > tops;)
+      if (!copies[start[at]].empty()) steps.push_back({start[at], false, copies[start[at]]});
+    // root's source overwrites root, and so on round to the one that root's held copy goes to
+    for (size_t at = 1; at < tops; ++at) steps.push_back({ring[at], false, copies[ring[at]]});
+    if (cycle) steps.push_back({root, true, copies[root]});
+    plan->components.push_back(std::move(steps));
+  }
+}
+
+kvq_status fork_impl(kvq_cache* c, const int32_t* src, const int32_t* dst, int32_t n, void* stream) {
+  if (!c) return fail(KVQ_EINVAL, "cache is NULL");
+  KVQ_TRY(check_device(c));
+  if (n < 0) return fail(KVQ_EINVAL, "n must not be negative (got %d)", n);
+  if (n == 0) return KVQ_OK;
+  if (!src || !dst) return fail(KVQ_EINVAL, "src / dst is NULL");
+  const int batch = c->cfg.batch;
+  std::vector<int32_t> from(batch, -1);
+  std::vector<char> is_dst(batch, 0);
+  for (int i = 0; i < n; ++i) {
+    if (src[i] < 0 || src[i] >= batch || dst[i] < 0 || dst[i] >= batch)
+      return fail(KVQ_EINVAL, "pair %d (%d to %d) is outside the %d sequences", i, src[i], dst[i], batch);
+    if (is_dst[dst[i]]) return fail(KVQ_EINVAL, "sequence %d is written twice", dst[i]);
+    is_dst[dst[i]] = 1;
+    if (c->total[src[i]] > c->cap[dst[i]])
+      return fail(KVQ_ECAPACITY, "the %d tokens of sequence %d exceed the capacity %lld of sequence %d", c->total[src[i]],
+                  src[i], (long long)c->cap[dst[i]], dst[i]);
+    if (src[i] != dst[i]) from[dst[i]] = src[i];
+  }
+  // copies of what holds tokens; an empty source only empties its copies
+  std::vector<int32_t> moved = from;
+  for (int32_t& s : moved)
+    if (s >= 0 && c->total[s] == 0) s = -1;
+  ForkPlan plan;
+  plan_fork(batch, moved, &plan);
+  for (const auto& steps : plan.components) {
+    size_t copies = 0;
+    for (const auto& s : steps) copies += s.dst.size();
+    if (steps.size() > kvq::kMaxForkSteps || copies > kvq::kMaxForkSteps)
+      return fail(KVQ_EUNSUPPORTED, "more than %d sequences depend on one another in one call", kvq::kMaxForkSteps);
+  }
+  const int64_t H = c->cfg.n_kv_heads, D = c->cfg.head_dim;
+  kvq::ForkParams p;
+  memset(&p, 0, sizeof p);
+  p.rcap = c->rcap;
+  p.layout = c->layout;
+  int64_t most_q = 0;
+  bool windows = false;
+  for (int b = 0; b < batch; ++b) {
+    if (moved[b] < 0) continue;
+    most_q = std::max<int64_t>(most_q, c->quantized[moved[b]]);
+    windows |= c->total[moved[b]] > c->quantized[moved[b]];
+  }
+  int64_t blocks = 0;
+  auto add = [&](void* base, int64_t seq_stride, int64_t unit_stride, int units, int grain, int64_t live_bytes,
+                 int live_tokens, int ring, int64_t bytes, bool by_layout = false) {
+    const int64_t cols = (bytes + grain - 1) / grain;
+    if (cols == 0) return;
+    kvq::ForkRegion& r = p.region[p.n_regions++];
+    r = {static_cast<uint8_t*>(base), seq_stride, unit_stride, live_bytes, live_tokens, ring, units, grain, by_layout,
+         cols, blocks};
+    blocks += units * ((cols + kvq::kForkCols - 1) / kvq::kForkCols);
+  };
+  if (c->segmented) {
+    auto rows = [&](void* base, int64_t row_bytes) {
+      add(base, H * c->seg.cap * row_bytes, c->seg.cap * row_bytes, (int)H, 16, row_bytes, 1, 0, most_q * row_bytes);
+    };
+    rows(c->seg.kcodes, c->seg.row_bytes);
+    rows(c->seg.vcodes, c->seg.row_bytes);
+    rows(c->seg.kscales, 4 * D);
+    rows(c->seg.vscales, 4);
+    add(c->seg.first, c->seg.cap * 4, 0, 1, 16, 4, 1, 0, most_q * 4);
+  } else if (c->paged) {
+    add(c->table, (int64_t)c->table_stride * 4, 0, 1, 4, 4, c->cfg.group, 0, most_q / c->cfg.group * 4);
+  } else {
+    add(c->pages, 0, 0, (int)H, 16, c->geom.page_bytes, c->cfg.group, 0, most_q / c->cfg.group * c->geom.page_bytes, true);
+  }
+  add(c->range, H * 8, 0, 1, 4, H * 8, 0, 0, H * 8);
+  const int64_t row = D * c->esize, ring = c->rcap * row;
+  for (void* base : {c->ring_k, c->ring_v})
+    add(base, H * ring, ring, (int)H, 16, 0, 0, (int)row, windows ? ring : 0);
+  if (blocks > (int64_t(1) << 31) - 1) return fail(KVQ_EUNSUPPORTED, "too much to copy in one launch");
+  // the counters and tables that the copies will have, from what all sequences hold before
+  std::vector<int32_t> total(batch), quantized(batch), last_flushed(batch);
+  std::vector<std::vector<int32_t>> blocks_of(batch), starts(batch);
+  for (int b = 0; b < batch; ++b) {
+    if (from[b] < 0) continue;
+    total[b] = c->total[from[b]];
+    quantized[b] = c->quantized[from[b]];
+    last_flushed[b] = c->last_flushed[from[b]];
+    blocks_of[b] = c->blocks[from[b]];
+    if (c->segmented) starts[b] = c->seg_starts[from[b]];
+  }
+  // components into launches
+  for (size_t at = 0; at < plan.components.size();) {
+    int components = 0, steps = 0, copies = 0;
+    for (; at < plan.components.size(); ++at) {
+      int more = 0;
+      for (const auto& s : plan.components[at]) more += (int)s.dst.size();
+      if (steps + (int)plan.components[at].size() > kvq::kMaxForkSteps || copies + more > kvq::kMaxForkSteps) break;
+      p.component[components++] = steps;
+      for (const auto& s : plan.components[at]) {
+        p.step[steps] = {s.src, copies, (int32_t)s.dst.size(), s.held, {c->total[s.src], c->quantized[s.src]}};
+        ++steps;
+        for (int32_t d : s.dst) p.dst[copies++] = d;
+      }
+    }
+    p.component[components] = steps;
+    const cudaError_t e = kvq::launch_fork(p, blocks, components, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "fork launch");
+    g_launches += 1;
+  }
+  for (int b = 0; b < batch; ++b)
+    for (int32_t blk : blocks_of[b]) ++c->block_users[blk];
+  for (int b = 0; b < batch; ++b) {
+    if (from[b] < 0) continue;
+    drop_blocks(c, b);
+    c->blocks[b] = std::move(blocks_of[b]);
+    if (c->segmented) c->seg_starts[b] = std::move(starts[b]);
+    c->total[b] = total[b];
+    c->quantized[b] = quantized[b];
+    c->last_flushed[b] = last_flushed[b];
+  }
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_fork(kvq_cache* c, const int32_t* src, const int32_t* dst, int32_t n, void* stream) {
+  try {
+    return fork_impl(c, src, dst, n, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(KVQ_ENOMEM, "out of host memory");
+  }
 }
 
 kvq_status kvq_pool_state(const kvq_cache* c, int64_t* free_blocks, int64_t* pool_blocks) {

@@ -258,6 +258,44 @@ struct RestoreParams {
   SeqCounters ctr[kMaxSeqsPerLaunch];
 };
 
+// Copy whole sequences of a cache (kvq_fork).  What a sequence holds lies in
+// regions; column x of a region is the same offset in every sequence, and no
+// other column of any sequence depends on it.  So a thread takes columns through
+// all steps of a component (sequences linked by pairs), in an order that reads
+// each sequence before it is overwritten.
+struct ForkRegion {
+  uint8_t* base;
+  int64_t seq_stride, unit_stride;  // bytes; ignored for group pages of a contiguous cache (SeqLayout)
+  int64_t live_bytes;               // of a unit: live_bytes per live_tokens quantized tokens, or
+  int32_t live_tokens;              // (live_tokens = 0) all live_bytes
+  int32_t ring;                     // rows of ``ring`` bytes of which the window's are live (else 0)
+  int32_t units;                    // per sequence
+  int32_t grain;                    // bytes of a column: 16 or 4
+  int32_t by_layout;
+  int64_t cols;                     // columns of a unit that any step copies
+  int64_t first_block;              // blocks of the launch before this region's
+};
+
+// Sequence src (or, flagged, the columns held in registers) is read, and
+// written to dst[first .. first + count) or, with count 0, held.
+struct ForkStep {
+  int32_t src, first, count, held;
+  SeqCounters ctr;                  // of the source
+};
+
+// Columns a fork block copies (every thread several at once).
+constexpr int kForkThreads = 128, kForkDepth = 4, kForkCols = kForkThreads * kForkDepth;
+constexpr int kMaxForkSteps = 512, kMaxForkRegions = 8;
+
+struct ForkParams {
+  int32_t n_regions, rcap;
+  const SeqLayout* layout;
+  ForkRegion region[kMaxForkRegions];
+  int32_t component[kMaxForkSteps + 1];  // first step of each (blockIdx.y), and the end
+  ForkStep step[kMaxForkSteps];
+  int32_t dst[kMaxForkSteps];
+};
+
 // The datawhale page's compare: quantize a Key/Value pair, restore, sum the
 // squared errors (kvq_compare).
 struct CompareParams {
@@ -300,6 +338,7 @@ bool decode_tc_supported(const DecodeParams& p);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t s);
 cudaError_t launch_decode_dense(const DecodeParams& p, cudaStream_t s, int* supported);
 cudaError_t launch_restore(const RestoreParams& p, cudaStream_t s);
+cudaError_t launch_fork(const ForkParams& p, int64_t blocks, int components, cudaStream_t s);
 // segmented caches: pass 1 (Key absmax, Value codes), pass 2 (Key codes), window copy
 cudaError_t launch_seg_flush(const SegFlushParams& p, int dtype, int64_t max_tokens, cudaStream_t s);
 cudaError_t launch_seg_window(const SegFlushParams& p, int dtype, cudaStream_t s);

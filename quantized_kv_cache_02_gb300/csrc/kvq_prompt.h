@@ -1,5 +1,5 @@
 // Internal definitions of the prompt operators (kvq_prompt_attention,
-// kvq_prompt_weights, kvq_evict): launch parameter blocks, the order in which
+// kvq_prompt_weights, kvq_evict) and of the cross attention (kvq_cross_attention): launch parameter blocks, the order in which
 // a launch takes its tiles, and the launchers.
 #pragma once
 
@@ -46,7 +46,50 @@ __host__ __device__ inline void prompt_tile(const PromptTiles& t, int64_t x, int
   *head = rem - *seq * t.Hkv;
 }
 
-struct PromptParams {
+// Tiles of a cross attention: sequence s (sorted by falling number of states) is
+// cut into nb[s] = ceil(q_len / step) blocks; its tiles, from first[s] on, are
+// its blocks of KV head 0, then of head 1 and so on.
+struct CrossSeq {
+  int32_t q_start, q_len;      // rows of q and out
+  int32_t kv_start, kv_len;    // rows of k and v
+};
+
+struct CrossTiles {
+  int32_t n_seqs, Hkv, step;
+  int64_t first[kMaxSeqsPerLaunch + 1];
+  CrossSeq seq[kMaxSeqsPerLaunch];
+};
+
+// What a tile's kernel needs to know: its sequence, KV head and block of tokens.
+struct Tile {
+  CrossSeq seq;
+  int head, level;
+};
+__host__ __device__ inline Tile tile_at(const PromptTiles& t, int64_t x) {
+  Tile r;
+  int s;
+  prompt_tile(t, x, &s, &r.head, &r.level);
+  r.seq = {t.seq[s].start, t.seq[s].len, t.seq[s].start, t.seq[s].len};
+  return r;
+}
+__host__ __device__ inline Tile tile_at(const CrossTiles& t, int64_t x) {
+  int lo = 0, hi = t.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.first[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  Tile r;
+  r.seq = t.seq[lo];
+  const int64_t off = x - t.first[lo];
+  const int nb = prompt_blocks(r.seq.q_len, t.step);
+  r.head = (int)(off / nb);
+  r.level = (int)(off - (int64_t)r.head * nb);
+  return r;
+}
+
+// What causal and cross attention share.
+struct AttentionParams {
   int32_t D, Hq, Hkv, g;
   float scale2;                // log2(e) / sqrt(D): scores are kept in base 2
   const void* q;               // element (token, head, c) at token * q_ts + head * q_hs + c
@@ -55,13 +98,23 @@ struct PromptParams {
   void* out;
   int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
   float* lse;                  // [Hq][n_tokens] (attention: written if non-null; weights: read)
-  float* weights;              // [Hkv][n_tokens]
-  int64_t n_tokens;
-  int64_t last;                // weights: queries counted back from each sequence's end
-  float lse_hi, lse_lo;        // weights: lse times their sum is in the scores' units
+  int64_t n_tokens;            // rows of q (and, causal, of k and v)
   int32_t split;               // CTAs of a cluster that share a tile (of queries, or a pair of key tiles)
   int32_t* status;
+};
+
+struct PromptParams : AttentionParams {
+  static constexpr bool kCausal = true;
+  float* weights;              // [Hkv][n_tokens]
+  int64_t last;                // weights: queries counted back from each sequence's end
+  float lse_hi, lse_lo;        // weights: lse times their sum is in the scores' units
   PromptTiles tiles;
+};
+
+struct CrossParams : AttentionParams {
+  static constexpr bool kCausal = false;
+  int64_t n_kv_tokens;         // rows of k and v
+  CrossTiles tiles;
 };
 
 struct EvictSeq {
@@ -118,6 +171,7 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int64_t tiles, int split, 
 
 // Launchers (return the launch's error code).
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
+cudaError_t launch_cross_simt(const CrossParams& p, int dtype, int64_t tiles, cudaStream_t s);
 // CTAs that share a tile of the CUDA-core attention
 int prompt_simt_split(int64_t tiles, int32_t max_len, int n_sm);
 cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);

@@ -11,7 +11,7 @@
 #include <new>
 #include <vector>
 
-#include "kvq_host.h"
+#include "kvq_args.h"
 #include "kvq_prompt.h"
 
 namespace kvq {
@@ -44,11 +44,13 @@ bool tma_map3(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_
 
 namespace {
 
+using kvq::check_floats;
+using kvq::check_on_device;
 using kvq::cuda_fail;
 using kvq::fail;
-
-constexpr int64_t kMaxTokens = int64_t(1) << 30;  // positions and tile ends stay within 32 bits
-constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
+using kvq::kMaxTiles;
+using kvq::kMaxTokens;
+using kvq::sm_count;
 
 int esize_of(const kvq_prompt* p) { return p->dtype == KVQ_BF16 ? 2 : 4; }
 
@@ -80,57 +82,16 @@ kvq_status check_prompt(const kvq_prompt* p, int64_t* total) {
   return KVQ_OK;
 }
 
-// A [tokens][heads][head_dim] tensor: strides in elements, 16-byte steps.
 kvq_status check_tensor(const kvq_prompt* p, const char* name, const void* ptr, int64_t ts, int64_t hs, int heads) {
-  if (!ptr || ((uintptr_t)ptr & 15u))
-    return fail(KVQ_EINVAL, "%s must be a non-NULL 16-byte aligned device pointer", name);
-  const int64_t step = 16 / esize_of(p);
-  if ((p->n_tokens > 1 && (ts < p->head_dim || ts % step)) || (heads > 1 && (hs < p->head_dim || hs % step)))
-    return fail(KVQ_EINVAL, "%s strides (token %lld, head %lld) must be multiples of %lld elements and at least head_dim",
-                name, (long long)ts, (long long)hs, (long long)step);
-  const int64_t most = (int64_t(1) << 40) / esize_of(p);
-  if ((p->n_tokens > 1 && ts >= most) || (heads > 1 && hs >= most))
-    return fail(KVQ_EUNSUPPORTED, "%s strides must be below 2^40 bytes", name);
-  return KVQ_OK;
+  return kvq::check_tensor(name, ptr, esize_of(p), p->n_tokens, heads, p->head_dim, ts, hs);
 }
 
-// No two of out's rows may share memory.
 kvq_status check_out(const kvq_prompt* p, const void* ptr) {
-  const int64_t ts = p->out_token_stride, hs = p->out_head_stride, d = p->head_dim;
-  const kvq_status st = check_tensor(p, "out", ptr, ts, hs, p->n_q_heads);
-  if (st != KVQ_OK) return st;
-  if (p->n_tokens > 1 && p->n_q_heads > 1 && hs * (p->n_q_heads - 1) + d > ts && ts * (p->n_tokens - 1) + d > hs)
-    return fail(KVQ_EINVAL, "out strides (token %lld, head %lld) make its rows overlap", (long long)ts, (long long)hs);
-  return KVQ_OK;
-}
-
-// Kernels launch on the current device: every tensor has to live there.
-kvq_status check_on_device(const char* name, const void* ptr) {
-  int cur = -1;
-  cudaError_t e = cudaGetDevice(&cur);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  cudaPointerAttributes attr;
-  e = cudaPointerGetAttributes(&attr, ptr);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes");
-  if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged)
-    return fail(KVQ_EINVAL, "%s is not device memory", name);
-  if (attr.type == cudaMemoryTypeDevice && attr.device != cur)
-    return fail(KVQ_EINVAL, "the current device is %d but %s lives on device %d", cur, name, attr.device);
-  return KVQ_OK;
-}
-
-kvq_status check_floats(const char* name, const void* ptr) {
-  if (!ptr || ((uintptr_t)ptr & 3u)) return fail(KVQ_EINVAL, "%s must be a non-NULL 4-byte aligned device pointer", name);
-  return check_on_device(name, ptr);
+  return kvq::check_out_tensor("out", ptr, esize_of(p), p->n_tokens, p->n_q_heads, p->head_dim, p->out_token_stride,
+                               p->out_head_stride);
 }
 
 kvq_status check_status_word(const kvq_prompt* p) { return p->status ? check_floats("status", p->status) : KVQ_OK; }
-
-#define KVQ_TRY(x)                       \
-  do {                                   \
-    const kvq_status st_ = (x);          \
-    if (st_ != KVQ_OK) return st_;       \
-  } while (0)
 
 // The sequences of the prompt that hold tokens, in launches of at most
 // kMaxSeqsPerLaunch, each sorted by falling length.
@@ -153,13 +114,6 @@ std::vector<std::vector<kvq::PromptSeq>> launches_of(const kvq_prompt* p) {
 // The tensor-core kernels' shapes.
 bool tensor_cores(const kvq_prompt* p) {
   return p->dtype == KVQ_BF16 && (p->head_dim == 64 || p->head_dim == 128);
-}
-
-kvq_status sm_count(int* n) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "cudaDeviceGetAttribute");
 }
 
 // Tiles of ``step`` tokens over the sequences; returns their number.

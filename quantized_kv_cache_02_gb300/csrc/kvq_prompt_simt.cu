@@ -72,7 +72,7 @@ __device__ __forceinline__ bool load_keys(float* dst, int stride, int cols, cons
 // Row r of a query tile is token tok0 + r / g, head h * g + r % g; rows past
 // the tile's tokens or the sequence are 0.
 template <typename T>
-__device__ __forceinline__ void load_queries(float* dst, int stride, const PromptParams& p, const T* q, int tok0,
+__device__ __forceinline__ void load_queries(float* dst, int stride, const AttentionParams& p, const T* q, int tok0,
                                              int tile_tok, int len, int h) {
   const int per = p.D / 4;
   for (int i = threadIdx.x; i < kPromptRows * per; i += kThreads) {
@@ -135,27 +135,27 @@ __device__ __forceinline__ float2 peer_load2(const float2* p, int rank) {
   return v;
 }
 
-// NC: 64-channel column groups of the output (D <= 64 NC).
-template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(const __grid_constant__ PromptParams p) {
+// NC: 64-channel column groups of the output (D <= 64 NC).  P: PromptParams, or
+// CrossParams, whose rows all see all of their sequence's states.
+template <typename T, int NC, typename P>
+__global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(const __grid_constant__ P p) {
   extern __shared__ __align__(16) float simt_smem[];
   constexpr int kStride = 64 * NC + 4;
   float* qs = simt_smem;                        // [64][kStride]
   float* ks = qs + kPromptRows * kStride;       // K, then V
   float* ps = ks + kPromptKeys * kStride;       // [64][kPStride]
-  int si, h, level;
   const int rank = blockIdx.x % p.split;  // clusters are ``split`` CTAs in a row
-  prompt_tile(p.tiles, blockIdx.x / p.split, &si, &h, &level);
-  const PromptSeq sq = p.tiles.seq[si];
-  const int tile_tok = p.tiles.step, tok0 = level * tile_tok;
-  const T* q = static_cast<const T*>(p.q) + (int64_t)sq.start * p.q_ts;
-  const T* k = static_cast<const T*>(p.k) + (int64_t)sq.start * p.k_ts + (int64_t)h * p.k_hs;
-  const T* v = static_cast<const T*>(p.v) + (int64_t)sq.start * p.v_ts + (int64_t)h * p.v_hs;
+  const Tile tile = tile_at(p.tiles, blockIdx.x / p.split);
+  const CrossSeq sq = tile.seq;
+  const int h = tile.head, tile_tok = p.tiles.step, tok0 = tile.level * tile_tok;
+  const T* q = static_cast<const T*>(p.q) + (int64_t)sq.q_start * p.q_ts;
+  const T* k = static_cast<const T*>(p.k) + (int64_t)sq.kv_start * p.k_ts + (int64_t)h * p.k_hs;
+  const T* v = static_cast<const T*>(p.v) + (int64_t)sq.kv_start * p.v_ts + (int64_t)h * p.v_hs;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   pdl_wait();
   pdl_release();
-  load_queries(qs, kStride, p, q, tok0, tile_tok, sq.len, h);
-  const int end = min(sq.len, tok0 + tile_tok);  // keys some row sees
+  load_queries(qs, kStride, p, q, tok0, tile_tok, sq.q_len, h);
+  const int end = P::kCausal ? min(sq.q_len, tok0 + tile_tok) : sq.kv_len;  // keys some row sees
   float2 o[NC][4][2];
   float m[4], l[4];
   int pos[4];
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int key = k0 + tx + 16 * j;
-        s[i][j] = key <= pos[i] && key < end ? s[i][j] * p.scale2 : -INFINITY;
+        s[i][j] = (!P::kCausal || key <= pos[i]) && key < end ? s[i][j] * p.scale2 : -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
 #pragma unroll
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(
     __syncthreads();  // K has been read; P is complete
     // A weight of 0 does not silence an infinite or NaN Value: in blocks with keys
     // that some row does not see they are taken out, and given back at the end.
-    if (k0 + kPromptKeys - 1 > tok0) dirty |= __syncthreads_or(load_keys<true>(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D));
+    if (P::kCausal && k0 + kPromptKeys - 1 > tok0) dirty |= __syncthreads_or(load_keys<true>(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D));
     else {
       load_keys<false>(ks, kStride, 64 * NC, v, p.v_ts, k0, end, p.D);
       __syncthreads();
@@ -257,12 +257,12 @@ __global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(
   }
   auto finish = [&](int r, int col, float4 sum, float mr, float lr, bool first) {  // row r, columns col .. col + 3
     const int t = r / p.g, head = h * p.g + r - t * p.g;
-    if (t >= tile_tok || tok0 + t >= sq.len) return;
-    const float inv = 1.f / lr;
-    T* dst = static_cast<T*>(p.out) + (int64_t)(sq.start + tok0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+    if (t >= tile_tok || tok0 + t >= sq.q_len) return;
+    const float inv = !P::kCausal && end == 0 ? 0.f : 1.f / lr;  // over no states: zeros, and lse minus infinity
+    T* dst = static_cast<T*>(p.out) + (int64_t)(sq.q_start + tok0 + t) * p.o_ts + (int64_t)head * p.o_hs;
     if (col < p.D) store4(dst + col, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
     if (p.lse && first)
-      p.lse[(int64_t)head * p.n_tokens + sq.start + tok0 + t] = (mr + log2f(lr)) * 0.69314718055994530942f;
+      p.lse[(int64_t)head * p.n_tokens + sq.q_start + tok0 + t] = (mr + log2f(lr)) * 0.69314718055994530942f;
   };
   if (p.split == 1) {
 #pragma unroll
@@ -290,12 +290,14 @@ __global__ void __launch_bounds__(kThreads, NC == 4 ? 1 : 2) prompt_simt_kernel(
     const int r = rank * rows + x / (16 * NC), col = 4 * (x % (16 * NC));
     float top = -INFINITY;
     for (int k = 0; k < p.split; ++k) top = fmaxf(top, peer_load2(ml + r, k).x);
+    // rank 0 holds key 0, if there is one: top is finite
+    const float base = !P::kCausal && top == -INFINITY ? 0.f : top;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     float lr = 0.f;
     for (int k = 0; k < p.split; ++k) {
       const float2 part = peer_load2(ml + r, k);
       const float4 v = peer_load4(ks + r * kStride + col, k);
-      const float a = exp2f(part.x - top);  // rank 0 holds key 0: top is finite
+      const float a = exp2f(part.x - base);
       lr = fmaf(part.y, a, lr);
       sum.x = fmaf(v.x, a, sum.x);
       sum.y = fmaf(v.y, a, sum.y);
@@ -369,21 +371,21 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const __grid_con
 // ``most``: the shared memory of the kernel's largest head_dim.  The limit is a
 // state of the kernel that all host threads share: set to one call's size, it
 // would refuse a larger call that another thread is about to launch.
-template <typename K>
-cudaError_t launch_sized(K kernel, size_t most, size_t smem, int64_t tiles, const PromptParams& p, cudaStream_t s) {
+template <typename K, typename P>
+cudaError_t launch_sized(K kernel, size_t most, size_t smem, int64_t tiles, const P& p, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, tiles, p.split, kThreads, smem, s, p);
 }
 
-template <typename T>
-cudaError_t launch_attention_t(const PromptParams& p, int64_t tiles, cudaStream_t s) {
+template <typename T, typename P>
+cudaError_t launch_attention_t(const P& p, int64_t tiles, cudaStream_t s) {
   auto smem = [](int nc) {
     return ((size_t)(kPromptRows + kPromptKeys) * (64 * nc + 4) + kPromptRows * kPStride) * sizeof(float);
   };
-  if (p.D <= 64) return launch_sized(prompt_simt_kernel<T, 1>, smem(1), smem(1), tiles, p, s);
-  if (p.D <= 128) return launch_sized(prompt_simt_kernel<T, 2>, smem(2), smem(2), tiles, p, s);
-  return launch_sized(prompt_simt_kernel<T, 4>, smem(4), smem(4), tiles, p, s);
+  if (p.D <= 64) return launch_sized(prompt_simt_kernel<T, 1, P>, smem(1), smem(1), tiles, p, s);
+  if (p.D <= 128) return launch_sized(prompt_simt_kernel<T, 2, P>, smem(2), smem(2), tiles, p, s);
+  return launch_sized(prompt_simt_kernel<T, 4, P>, smem(4), smem(4), tiles, p, s);
 }
 
 }  // namespace
@@ -395,6 +397,10 @@ int prompt_simt_split(int64_t tiles, int32_t max_len, int n_sm) {
 }
 
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s) {
+  return dtype == 0 ? launch_attention_t<__nv_bfloat16>(p, tiles, s) : launch_attention_t<float>(p, tiles, s);
+}
+
+cudaError_t launch_cross_simt(const CrossParams& p, int dtype, int64_t tiles, cudaStream_t s) {
   return dtype == 0 ? launch_attention_t<__nv_bfloat16>(p, tiles, s) : launch_attention_t<float>(p, tiles, s);
 }
 
