@@ -115,7 +115,10 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
   p.Hq = c->n_q_heads;
   p.Hkv = c->n_kv_heads;
   p.g = c->n_q_heads / c->n_kv_heads;
-  p.scale2 = (float)(1.4426950408889634 / std::sqrt((double)d));
+  const bool tc = c->dtype == KVQ_BF16 && (d == 64 || d == 128) && any_kv;
+  // (the tensor cores: d / 16 partial sums that grow evenly)
+  p.scale2 = (float)(1.4426950408889634 / std::sqrt((double)d) *
+                     (tc ? 1.0 + kvq::rounding_loss((d / 16 + 1) / 2.0) : 1.0));
   p.q = q;
   p.k = k;
   p.v = v;
@@ -133,7 +136,7 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
   p.n_kv_tokens = c->n_kv_tokens;
   p.status = c->status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int step = kvq::kPromptRows / p.g;
+  const int step = tc ? kvq::prompt_tc_tokens(p.g) : kvq::kPromptRows / p.g;
   for (size_t at = 0; at < seqs.size(); at += kvq::kMaxSeqsPerLaunch) {
     const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, seqs.size() - at);
     if (fill_tiles(seqs, at, n, p.Hkv, step, &p.tiles) > kMaxTiles / 4)
@@ -142,8 +145,9 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
   for (size_t at = 0; at < seqs.size(); at += kvq::kMaxSeqsPerLaunch) {
     const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, seqs.size() - at);
     const int64_t tiles = fill_tiles(seqs, at, n, p.Hkv, step, &p.tiles);
-    p.split = kvq::prompt_simt_split(tiles, p.tiles.seq[0].kv_len, n_sm);
-    const cudaError_t e = kvq::launch_cross_simt(p, c->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
+    p.split = tc ? 1 : kvq::prompt_simt_split(tiles, p.tiles.seq[0].kv_len, n_sm);
+    const cudaError_t e = tc ? kvq::launch_cross_tc(p, tiles, n_sm, s)
+                             : kvq::launch_cross_simt(p, c->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
     if (e != cudaSuccess) return cuda_fail(e, "cross attention launch");
     kvq::count_launches(1);
   }

@@ -1,0 +1,466 @@
+// Cross attention on the fifth-generation tensor cores: bf16, head_dim 64 or 128,
+// sequences of many queries (kvq_cross_attention).
+//
+// A row is a (token, query head) pair of one KV head, token major.  A CTA holds
+// two tiles of 128 rows (floor(128 / g) tokens each) and walks the states in blocks
+// of 128, both tiles on the same Key and Value tile:
+//
+//   S_i = Q_i K^T       128 x 128, fp32 in tensor memory (Q, K from shared memory)
+//   P_i = 2^(S_i c - m) bf16, in tensor memory
+//   O_i += P_i V        128 x d, fp32 in tensor memory (P from tensor memory)
+//
+// Warps 0-3 and 4-7 run the softmax of tile 0 and 1, one row a thread; warp 8
+// issues the MMAs, warp 9 the TMA copies (two more fill the warpgroup, whose registers
+// go to the softmax).  Encoders' states are few (a text's 512 are four blocks), so what
+// surrounds the blocks counts: the CTAs stay and take item after item, and the ends
+// overlap.  The next item's queries and first states are copied while the last
+// blocks run, its first Q K^T follows a tile's last P V at once, and a tile's
+// output leaves (through shared memory of its own) under the other tile's MMAs.
+// Tensor memory, the running maximum that moves only past 2^8, and what is rounded
+// where are as in the causal kernel (kvq_prompt_tc.cu).
+// ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d)) V.)
+
+#include <cfloat>
+
+#include "kvq_prompt.h"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kTcThreads = 384;
+// Registers a thread after the split of the launch's 3 x 168: a softmax thread
+// holds a whole row of scores.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr float kSlack = 8.f;
+
+template <int D>
+struct TcLayout {
+  static constexpr int kSlots = D == 128 ? 4 : 8;         // Key and Value tiles in flight
+  static constexpr uint32_t kChunk = 128 * 128;           // 128 rows of 64 channels
+  static constexpr uint32_t kTile = kChunk * (D / 64);    // a Q, K or V tile
+  static constexpr uint32_t kStageWarp = 32 * 128;        // 32 rows of 64 output channels
+  static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kStage = kRing + kSlots * kTile, kBars = kStage + 8 * kStageWarp;
+  // barriers: full and empty per slot, the end, then per tile: Q full, Q empty, S, P (two halves), O, S read
+  static constexpr int kNBars = 2 * kSlots + 1 + 14;
+  static constexpr bool kApart = D == 64;                 // P beside S, not over it
+  static constexpr size_t kSmem = kBars + kNBars * 8 + 32 + 1024;  // + alignment
+  // S_i at 128 i, O_i at 256 + D i, P_i over S_i or at 384 + 64 i
+  static constexpr uint32_t kColS = 0, kColO = 256, kColP = kApart ? 384 : 0, kStepP = kApart ? 64 : 128;
+};
+
+struct TcMaps {
+  CUtensorMap q, k, v;
+};
+
+// An item: one KV head of one sequence, the tokens of two tiles.
+struct Item {
+  CrossSeq seq;
+  int head, tok0, n;   // first token of tile 0; blocks of states
+  bool two;            // tile 1 has tokens
+};
+
+__device__ __forceinline__ Item item_at(const CrossParams& p, int x) {
+  const Tile t = tile_at(p.tiles, x);
+  Item r;
+  r.seq = t.seq;
+  r.head = t.head;
+  r.tok0 = t.level * p.tiles.step;
+  r.n = (t.seq.kv_len + kKeys - 1) / kKeys;
+  r.two = r.tok0 + p.tiles.step / 2 < t.seq.q_len;
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ TcMaps maps, int n_items) {
+  using L = TcLayout<D>;
+  extern __shared__ uint8_t tc_raw[];
+  uint8_t* smem = tc_raw + ((1024u - (smem_u32(tc_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kSlots;
+  const uint32_t bar_end = bar_empty + 8 * L::kSlots, bar_q = bar_end + 8, bar_qfree = bar_q + 16,
+                 bar_s = bar_qfree + 16, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  const int tile_tok = p.tiles.step / 2;  // tokens of a tile
+
+  if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
+  if (t == 32 * kCopyWarp) {
+    *abort = 0;
+    for (int s = 0; s < L::kSlots; ++s) {
+      bar_init(bar_full + 8 * s, 1);
+      bar_init(bar_empty + 8 * s, 1);
+    }
+    bar_init(bar_end, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar_q + 8 * i, 1);
+      bar_init(bar_qfree + 8 * i, 1);
+      bar_init(bar_s + 8 * i, 1);
+      bar_init(bar_p + 16 * i, 4);  // a warp arrives once, by one lane
+      bar_init(bar_p + 16 * i + 8, 4);
+      bar_init(bar_o + 8 * i, 1);
+      bar_init(bar_r + 8 * i, 4);
+    }
+    bar_init_fence();
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *tslot;
+  pdl_wait();
+  pdl_release();
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+      // ============ copies (lane 0): per item Q_0, Q_1, then K_0, V_0, K_1, V_1 ... ====
+      if (lane == 0) {
+        uint32_t ring = 0, n_q[2] = {0, 0};
+        bool ok = true;
+        for (int x = blockIdx.x; x < n_items && ok; x += gridDim.x) {
+          const Item it = item_at(p, x);
+          if (it.n == 0) continue;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || (i == 1 && !it.two)) break;
+            if (n_q[i] > 0 && !(ok = bar_wait(bar_qfree + 8 * i, (n_q[i] - 1) & 1u, abort))) break;
+            ++n_q[i];
+            bar_expect(bar_q + 8 * i, (uint32_t)(tile_tok * p.g) * 128u * (D / 64));
+            for (int c = 0; c < D / 64; ++c)
+              tma_load3(sbase + L::kQ + i * L::kTile + c * L::kChunk, &maps.q, 64 * c, it.head * p.g,
+                        it.seq.q_start + it.tok0 + i * tile_tok, bar_q + 8 * i);
+          }
+          for (int b = 0; b < 2 * it.n && ok; ++b) {
+            const uint32_t s = ring % L::kSlots;
+            if (ring >= L::kSlots && !(ok = bar_wait(bar_empty + 8 * s, (ring / L::kSlots - 1) & 1u, abort))) break;
+            ++ring;
+            bar_expect(bar_full + 8 * s, L::kTile);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load3(sbase + L::kRing + s * L::kTile + c * L::kChunk, b & 1 ? &maps.v : &maps.k, 64 * c,
+                        it.seq.kv_start + (b >> 1) * kKeys, it.head, bar_full + 8 * s);
+          }
+        }
+        if (!ok) {
+          *abort = 1;
+          if (p.status) atomicOr(p.status, kStatusPromptTimeout);
+        }
+        // nothing in flight when the CTA ends
+        for (uint32_t r = ring > L::kSlots ? ring - L::kSlots : 0; r < ring; ++r)
+          bar_drain(bar_full + 8 * (r % L::kSlots), (r / L::kSlots) & 1u);
+        for (int i = 0; i < 2; ++i)
+          if (n_q[i] > 0) bar_drain(bar_q + 8 * i, (n_q[i] - 1) & 1u);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ============ MMAs, all issued by one lane ======================================
+      // With P over S, the next Q K^T overwrites P right behind the P V that reads it; a
+      // tcgen05.fence orders the two (different accumulators have no order of their own).
+      // Every wait is the whole warp's: its lanes never drift apart, whose waits for a
+      // phase could then miss it.
+      constexpr uint32_t idesc_s = bf16_idesc(kRows, kKeys, false), idesc_o = bf16_idesc(kRows, D, true);
+      const bool one = elect_one();
+      uint32_t ring = 0;                                  // of the current item's K_0
+      uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_r[2] = {0, 0};
+      bool ok = true;
+      auto landed = [&](uint32_t r) { return warp_wait(bar_full + 8 * (r % L::kSlots), (r / L::kSlots) & 1u, abort); };
+      // S_i of the block whose Keys are ring tile r; first: of an item (its queries have to be there)
+      auto scores = [&](int i, uint32_t r, bool first, bool last, bool end_of_k) {
+        if (first && !(ok = ok && warp_wait(bar_q + 8 * i, n_q[i]++ & 1u, abort))) return;
+        if (!(ok = ok && landed(r))) return;
+        tm_fence_after();
+        const uint32_t kaddr = sbase + L::kRing + (r % L::kSlots) * L::kTile;
+        const uint64_t a = sw128_desc(sbase + L::kQ + i * L::kTile, 0), b = sw128_desc(kaddr, 0);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
+          if (one) mma_ss(tm + L::kColS + 128 * i, a + off, b + off, idesc_s, ks > 0);
+        }
+        if (one) {
+          mma_commit(bar_s + 8 * i);
+          if (last) mma_commit(bar_qfree + 8 * i);
+          if (end_of_k) mma_commit(bar_empty + 8 * (r % L::kSlots));
+        }
+      };
+      // the first item with states from x on, or past the end
+      struct Brief {
+        int n, kv_len;
+        bool two;
+      };
+      auto find = [&](int x, Brief* b) {
+        for (; x < n_items; x += gridDim.x) {
+          const Item it = item_at(p, x);
+          *b = {it.n, it.seq.kv_len, it.two};
+          if (it.n > 0) break;
+        }
+        return x;
+      };
+      Brief cur, next;
+      int x = find(blockIdx.x, &cur);
+      if (x < n_items) {
+        scores(0, 0, true, cur.n == 1, !cur.two);
+        if (ok && cur.two) scores(1, 0, true, cur.n == 1, true);
+      }
+      while (x < n_items && ok) {
+        const int after = find(x + gridDim.x, &next);
+        const bool more = after < n_items;
+        const int rest = cur.kv_len - (cur.n - 1) * kKeys;
+        for (int j = 0; j < cur.n && ok; ++j) {
+          const bool end = j + 1 == cur.n;
+          // the scores that follow tile i's block j: of the next block, or of the next item
+          auto ahead = [&](int i) {
+            const uint32_t r = ring + 2 * (j + 1);
+            if (!end) {
+              if (i == 0 || cur.two) scores(i, r, false, j + 2 == cur.n, i == 1 || !cur.two);
+            } else if (more && (i == 0 || next.two)) {
+              scores(i, r, true, next.n == 1, i == 1 || !next.two);
+            }
+          };
+          if (L::kApart) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok) break;
+              // the rows have been read (every block's, so that no phase is missed)
+              if ((i == 0 || cur.two) && !(ok = warp_wait(bar_r + 8 * i, n_r[i]++ & 1u, abort))) break;
+              ahead(i);
+            }
+          }
+          const uint32_t rv = ring + 2 * j + 1, vslot = rv % L::kSlots;
+          const uint64_t b = sw128_desc(sbase + L::kRing + vslot * L::kTile, L::kChunk);
+          const int steps = end ? (rest + 15) / 16 : 8;
+          if (ok) ok = landed(rv);
+          if (end && rest % 16 != 0) {
+            // Values behind the last state, in the last k-step of 16: other sequences', whose
+            // infinities and NaN a weight of 0 does not silence
+            for (int c = 0; c < D / 64; ++c) {
+              uint4* rows = reinterpret_cast<uint4*>(smem + L::kRing + vslot * L::kTile + c * L::kChunk);
+              for (int y = 8 * rest + lane; y < 8 * ((rest + 15) & ~15); y += 32) rows[y] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            async_proxy_fence();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok) break;
+            if (i == 0 || cur.two) {
+              auto values = [&](int ks) {
+                if (one)
+                  mma_ts(tm + L::kColO + D * i, tm + L::kColP + L::kStepP * i + 8 * ks, b + ks * (2048 >> 4), idesc_o,
+                         j > 0 || ks > 0);
+              };
+              if (!(ok = warp_wait(bar_p + 16 * i, n_p[i] & 1u, abort))) break;
+              tm_fence_after();
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                if (ks < steps) values(ks);
+              if (!(ok = warp_wait(bar_p + 16 * i + 8, n_p[i]++ & 1u, abort))) break;
+              tm_fence_after();
+#pragma unroll
+              for (int ks = 4; ks < 8; ++ks)
+                if (ks < steps) values(ks);
+              if (one && (L::kApart || end)) mma_commit(bar_o + 8 * i);
+            }
+            if (!L::kApart) {
+              tm_fence_before();
+              ahead(i);
+            }
+          }
+          if (ok && one) mma_commit(bar_empty + 8 * vslot);
+        }
+        ring += 2 * cur.n;
+        cur = next;
+        x = after;
+      }
+      if (!ok) {
+        *abort = 1;
+        if (one && p.status) atomicOr(p.status, kStatusPromptTimeout);
+      }
+      // no MMA in flight, and no arrival to come, when the CTA ends
+      __syncwarp();
+      if (one) {
+        mma_commit(bar_end);
+        bar_drain(bar_end, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ============ softmax: tile i, one row a thread ===================================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int i = warp >> 2, r = t & 127;
+    const int tt = r / p.g, member = r - tt * p.g;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tm + L::kColS + 128 * i + lanes, to = tm + L::kColO + D * i + lanes,
+                   tp = tm + L::kColP + L::kStepP * i + lanes;
+    const float2 sc = make_float2(p.scale2, p.scale2);
+    uint8_t* stage = smem + L::kStage + warp * L::kStageWarp;
+    uint32_t n_s = 0, n_o = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; x < n_items && ok; x += gridDim.x) {
+      int n, kv_len;
+      bool warp_live;
+      {
+        const Item it = item_at(p, x);
+        if (i == 1 && !it.two) continue;
+        n = it.n;
+        kv_len = it.seq.kv_len;
+        warp_live = __any_sync(0xffffffffu, tt < tile_tok && it.tok0 + i * tile_tok + tt < it.seq.q_len);
+      }
+      float m = -FLT_MAX, l = 0.f;  // (not -INFINITY: scores of minus infinity may come first)
+      for (int j = 0; j < n; ++j, ++n_s) {
+        if (!(ok = warp_wait(bar_s + 8 * i, n_s & 1u, abort))) break;
+        if (warp_live) {
+          tm_fence_after();
+          float s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tm_ld32(ts + 32 * c, s + 32 * c);
+          tm_wait_ld();
+          if (L::kApart) {
+            tm_fence_before();
+            warp_arrive(bar_r + 8 * i);
+          }
+          const int limit = kv_len - j * kKeys;  // states of the block
+          if (limit < kKeys) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= limit) s[c] = -INFINITY;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < 124; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
+          const bool up = top > m + kSlack;
+          if (L::kApart && j > 0) {  // the last block's P V is done with P and with O
+            if (!(ok = warp_wait(bar_o + 8 * i, n_o++ & 1u, abort))) break;
+            tm_fence_after();
+          }
+          if (__any_sync(0xffffffffu, up)) {
+            const float a = up ? ex2(m - top) : 1.f;
+            if (up) m = top;
+            l *= a;
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tm_ld32(to + 32 * c, o);
+                tm_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= a;
+                tm_st32(to + 32 * c, o);
+              }
+            }
+          }
+          const float2 nm = make_float2(-m, -m);
+          float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 128; c += 64) {
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              float2 y = fma2(make_float2(s[c + e], s[c + e + 1]), sc, nm);
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], y);
+              w[e / 2] = pack_bf16(y.x, y.y);
+            }
+            tm_st32(tp + c / 2, reinterpret_cast<const float*>(w));
+            tm_wait_st();
+            tm_fence_before();
+            if (c == 0) warp_arrive(bar_p + 16 * i);  // the first 64 states' weights: their P V may start
+          }
+          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          l += sum[0].x + sum[0].y;
+        } else {
+          if (L::kApart) {
+            // like the others, so that no arrival counts for the block before
+            warp_arrive(bar_r + 8 * i);
+            if (j > 0 && !(ok = warp_wait(bar_o + 8 * i, n_o++ & 1u, abort))) break;
+          }
+          warp_arrive(bar_p + 16 * i);
+        }
+        warp_arrive(bar_p + 16 * i + 8);
+      }
+      if (ok && n > 0) ok = warp_wait(bar_o + 8 * i, n_o++ & 1u, abort);
+      if (!ok) break;
+      if (!warp_live) continue;
+      tm_fence_after();
+      const Item it = item_at(p, x);  // (again: kept over the blocks it would cost them registers)
+      const int pos = it.tok0 + i * tile_tok + tt, head = it.head * p.g + member;
+      const bool live = tt < tile_tok && pos < it.seq.q_len;
+      const float inv = 1.f / l;
+      __nv_bfloat16* dst =
+          static_cast<__nv_bfloat16*>(p.out) + (int64_t)(it.seq.q_start + pos) * p.o_ts + (int64_t)head * p.o_hs;
+      // 64 channels at a time through shared memory, 16-byte pieces swizzled by row,
+      // so that the warp stores whole rows
+      const uint32_t rows_live = __ballot_sync(0xffffffffu, live);
+#pragma unroll 1
+      for (int half = 0; half < D / 64; ++half) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float o[32];
+          tm_ld32(to + 64 * half + 32 * c, o);  // (without states anything, and not used)
+          tm_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = it.n > 0 ? o[e] * inv : 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((4 * c + e / 8) ^ (lane & 7)) * 16) =
+                make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
+                           pack_bf16(o[e + 6], o[e + 7]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int y = lane; y < 32 * 8; y += 32) {
+          const int row = y / 8, c = y % 8;
+          const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (c ^ (row & 7)) * 16);
+          if (rows_live >> row & 1u) *reinterpret_cast<uint4*>(at + 128 * half + 16 * c) = v;
+        }
+        __syncwarp();
+      }
+      tm_fence_before();
+      if (live && p.lse)
+        p.lse[(int64_t)head * p.n_tokens + it.seq.q_start + pos] =
+            it.n > 0 ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+    }
+    if (!ok) {
+      *abort = 1;
+      if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tm_free<512>(tm);
+  }
+}
+
+template <int D>
+cudaError_t launch_tc(const CrossParams& p, const TcMaps& maps, int64_t tiles, int n_sm, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)TcLayout<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(cross_tc_kernel<D>, dim3((unsigned)(tiles < n_sm ? tiles : n_sm)), dim3(kTcThreads),
+                    TcLayout<D>::kSmem, s, p, maps, (int)tiles);
+}
+
+}  // namespace
+
+cudaError_t launch_cross_tc(const CrossParams& p, int64_t tiles, int n_sm, cudaStream_t s) {
+  TcMaps maps;
+  // dims (channel, head, token) for the queries, (channel, token, head) for Keys and Values
+  if (!tma_map3(&maps.q, p.q, p.D, p.Hq, p.n_tokens, p.q_hs, p.q_ts, p.g, kRows / p.g) ||
+      !tma_map3(&maps.k, p.k, p.D, p.n_kv_tokens, p.Hkv, p.k_ts, p.k_hs, kKeys, 1) ||
+      !tma_map3(&maps.v, p.v, p.D, p.n_kv_tokens, p.Hkv, p.v_ts, p.v_hs, kKeys, 1))
+    return cudaErrorInvalidValue;
+  return p.D == 128 ? launch_tc<128>(p, maps, tiles, n_sm, s) : launch_tc<64>(p, maps, tiles, n_sm, s);
+}
+
+}  // namespace kvq

@@ -188,6 +188,13 @@ int prompt_tc_tokens(int g);
 void weights_tc_plan(int64_t pairs, int64_t most_tokens, int g, int n_sm, int* chunk, int* split);
 cudaError_t launch_weights_tc(const PromptParams& p, int64_t tiles, cudaStream_t s);
 
+// the tensor-core cross attention (bf16, head_dim 64 or 128): tiles of
+// prompt_tc_tokens(g) tokens, taken by at most n_sm CTAs
+cudaError_t launch_cross_tc(const CrossParams& p, int64_t tiles, int n_sm, cudaStream_t s);
+
+// what the tensor cores' rounding takes from a score
+double rounding_loss(double sums);
+
 // TMA map of a bf16 tensor (channel, d1, d2) with strides s1, s2 (elements) and
 // boxes of 64 channels x b1 x b2, 128-byte swizzled; false if the driver refuses it.
 bool tma_map3(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1,
