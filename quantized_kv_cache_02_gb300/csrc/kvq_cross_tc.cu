@@ -32,7 +32,7 @@ constexpr int kRows = 128, kKeys = 128;
 constexpr int kMmaWarp = 8, kCopyWarp = 9, kTcThreads = 384;
 // Registers a thread after the split of the launch's 3 x 168: a softmax thread
 // holds a whole row of scores.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr float kSlack = 8.f;
 
 template <int D>
@@ -45,7 +45,8 @@ struct TcLayout {
   // barriers: full and empty per slot, the end, then per tile: Q full, Q empty, S, P (two halves), O, S read
   static constexpr int kNBars = 2 * kSlots + 1 + 14;
   static constexpr bool kApart = D == 64;                 // P beside S, not over it
-  static constexpr size_t kSmem = kBars + kNBars * 8 + 32 + 1024;  // + alignment
+  static constexpr uint32_t kBriefs = kBars + kNBars * 8 + 8;     // behind the tensor memory's address and the abort word
+  static constexpr size_t kSmem = kBriefs + 16 + 1024;    // + alignment
   // S_i at 128 i, O_i at 256 + D i, P_i over S_i or at 384 + 64 i
   static constexpr uint32_t kColS = 0, kColO = 256, kColP = kApart ? 384 : 0, kStepP = kApart ? 64 : 128;
 };
@@ -72,6 +73,13 @@ __device__ __forceinline__ Item item_at(const CrossParams& p, int x) {
   return r;
 }
 
+// What the MMA warp needs of an item, written by the copy warp before the
+// item's first copy: registers that the MMA warp does not have.
+struct Brief {
+  int n;
+  uint32_t info;  // states of the last block, tile 1 has tokens (bit 8), another item follows (bit 9)
+};
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ TcMaps maps, int n_items) {
@@ -85,6 +93,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                  bar_s = bar_qfree + 16, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  Brief* briefs = reinterpret_cast<Brief*>(smem + L::kBriefs);
   const int tile_tok = p.tiles.step / 2;  // tokens of a tile
 
   if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
@@ -120,14 +129,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) {
         uint32_t ring = 0, n_q[2] = {0, 0};
         bool ok = true;
-        for (int x = blockIdx.x; x < n_items && ok; x += gridDim.x) {
-          const Item it = item_at(p, x);
-          if (it.n == 0) continue;
+        // the first item with states from x on, or past the end
+        auto find = [&](int x, Item* it) {
+          for (; x < n_items; x += gridDim.x) {
+            *it = item_at(p, x);
+            if (it->n > 0) break;
+          }
+          return x;
+        };
+        Item it, next;
+        for (int x = find(blockIdx.x, &it), after, k = 0; x < n_items && ok; x = after, it = next, ++k) {
+          after = find(x + gridDim.x, &next);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!ok || (i == 1 && !it.two)) break;
             if (n_q[i] > 0 && !(ok = bar_wait(bar_qfree + 8 * i, (n_q[i] - 1) & 1u, abort))) break;
             ++n_q[i];
+            // (the item before the last, whose place it takes, is done: its last Q K^T was)
+            if (i == 0)
+              briefs[k & 1] = {it.n, (uint32_t)(it.seq.kv_len - (it.n - 1) * kKeys) | (it.two ? 0x100u : 0u) |
+                                         (after < n_items ? 0x200u : 0u)};
             bar_expect(bar_q + 8 * i, (uint32_t)(tile_tok * p.g) * 128u * (D / 64));
             for (int c = 0; c < D / 64; ++c)
               tma_load3(sbase + L::kQ + i * L::kTile + c * L::kChunk, &maps.q, 64 * c, it.head * p.g,
@@ -158,79 +179,66 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ============ MMAs, all issued by one lane ======================================
       // With P over S, the next Q K^T overwrites P right behind the P V that reads it; a
       // tcgen05.fence orders the two (different accumulators have no order of their own).
-      // Every wait is the whole warp's: its lanes never drift apart, whose waits for a
-      // phase could then miss it.
+      // The lanes wait each for itself and meet before anything is issued that lets a phase
+      // that they waited for be followed by its next: a lane that lags behind that
+      // would miss the one it waits for.
       constexpr uint32_t idesc_s = bf16_idesc(kRows, kKeys, false), idesc_o = bf16_idesc(kRows, D, true);
       const bool one = elect_one();
+      auto meet = [](bool ok) -> bool { return __all_sync(0xffffffffu, ok); };
       uint32_t ring = 0;                                  // of the current item's K_0
-      uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_r[2] = {0, 0};
+      uint32_t ph_q = 0, ph_p = 0, ph_r = 0;              // the phase to wait for, bit i for tile i
       bool ok = true;
-      auto landed = [&](uint32_t r) { return warp_wait(bar_full + 8 * (r % L::kSlots), (r / L::kSlots) & 1u, abort); };
-      // S_i of the block whose Keys are ring tile r; first: of an item (its queries have to be there)
-      auto scores = [&](int i, uint32_t r, bool first, bool last, bool end_of_k) {
-        if (first && !(ok = ok && warp_wait(bar_q + 8 * i, n_q[i]++ & 1u, abort))) return;
-        if (!(ok = ok && landed(r))) return;
-        tm_fence_after();
-        const uint32_t kaddr = sbase + L::kRing + (r % L::kSlots) * L::kTile;
-        const uint64_t a = sw128_desc(sbase + L::kQ + i * L::kTile, 0), b = sw128_desc(kaddr, 0);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
-          if (one) mma_ss(tm + L::kColS + 128 * i, a + off, b + off, idesc_s, ks > 0);
-        }
-        if (one) {
-          mma_commit(bar_s + 8 * i);
-          if (last) mma_commit(bar_qfree + 8 * i);
-          if (end_of_k) mma_commit(bar_empty + 8 * (r % L::kSlots));
-        }
-      };
-      // the first item with states from x on, or past the end
-      struct Brief {
-        int n, kv_len;
-        bool two;
-      };
-      auto find = [&](int x, Brief* b) {
-        for (; x < n_items; x += gridDim.x) {
-          const Item it = item_at(p, x);
-          *b = {it.n, it.seq.kv_len, it.two};
-          if (it.n > 0) break;
-        }
-        return x;
-      };
-      Brief cur, next;
-      int x = find(blockIdx.x, &cur);
-      if (x < n_items) {
-        scores(0, 0, true, cur.n == 1, !cur.two);
-        if (ok && cur.two) scores(1, 0, true, cur.n == 1, true);
-      }
-      while (x < n_items && ok) {
-        const int after = find(x + gridDim.x, &next);
-        const bool more = after < n_items;
-        const int rest = cur.kv_len - (cur.n - 1) * kKeys;
-        for (int j = 0; j < cur.n && ok; ++j) {
+      // Block -1 stands for the end of an item before the first (items come by falling
+      // number of states).
+      Brief cur = {0, item_at(p, blockIdx.x).n > 0 ? 0x200u : 0u}, next = {};
+      int j = -1, begun = 0;
+      for (;;) {
+        const int rest = cur.info & 0xff;
+        for (; j < cur.n && ok; ++j) {
           const bool end = j + 1 == cur.n;
+          const uint32_t rk = ring + 2 * (j + 1), kslot = rk % L::kSlots;
+          const uint64_t bk = sw128_desc(sbase + L::kRing + kslot * L::kTile, 0);
           // the scores that follow tile i's block j: of the next block, or of the next item
           auto ahead = [&](int i) {
-            const uint32_t r = ring + 2 * (j + 1);
-            if (!end) {
-              if (i == 0 || cur.two) scores(i, r, false, j + 2 == cur.n, i == 1 || !cur.two);
-            } else if (more && (i == 0 || next.two)) {
-              scores(i, r, true, next.n == 1, i == 1 || !next.two);
+            if (!ok || (end && !(cur.info & 0x200u))) return;
+            if (i == 1 && !((end ? next.info : cur.info) & 0x100u)) return;
+            if (end) {
+              ok = bar_wait(bar_q + 8 * i, ph_q >> i & 1u, abort);
+              ph_q ^= 1u << i;
+              if (i == 0) next = briefs[begun++ & 1];
             }
+            const bool two = (end ? next.info : cur.info) & 0x100u, last = end ? next.n == 1 : j + 2 == cur.n;
+            if (i == 0) ok = ok && bar_wait(bar_full + 8 * kslot, (rk / L::kSlots) & 1u, abort);
+            if (!(ok = meet(ok))) return;
+            uint32_t qaddr;  // (computed here: descriptors kept over the blocks would be spilled)
+            asm volatile("add.u32 %0, %1, %2;" : "=r"(qaddr) : "r"(sbase), "r"(L::kQ + i * L::kTile));
+            const uint64_t a = sw128_desc(qaddr, 0);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks / 4) * (L::kChunk >> 4) + (ks % 4) * 2;
+              if (one) mma_ss(tm + L::kColS + 128 * i, a + off, bk + off, idesc_s, ks > 0);
+            }
+            if (one) mma_commit(bar_s + 8 * i);
+            if (one && last) mma_commit(bar_qfree + 8 * i);
+            if (one && (i == 1 || !two)) mma_commit(bar_empty + 8 * kslot);
           };
-          if (L::kApart) {
+          if (L::kApart || j < 0) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (!ok) break;
               // the rows have been read (every block's, so that no phase is missed)
-              if ((i == 0 || cur.two) && !(ok = warp_wait(bar_r + 8 * i, n_r[i]++ & 1u, abort))) break;
+              if (L::kApart && j >= 0 && (i == 0 || cur.info & 0x100u)) {
+                ok = meet(ok && bar_wait(bar_r + 8 * i, ph_r >> i & 1u, abort));
+                ph_r ^= 1u << i;
+                tm_fence_after();
+              }
               ahead(i);
             }
           }
+          if (j < 0) continue;
           const uint32_t rv = ring + 2 * j + 1, vslot = rv % L::kSlots;
-          const uint64_t b = sw128_desc(sbase + L::kRing + vslot * L::kTile, L::kChunk);
+          const uint64_t bv = sw128_desc(sbase + L::kRing + vslot * L::kTile, L::kChunk);
           const int steps = end ? (rest + 15) / 16 : 8;
-          if (ok) ok = landed(rv);
+          ok = ok && bar_wait(bar_full + 8 * vslot, (rv / L::kSlots) & 1u, abort);
           if (end && rest % 16 != 0) {
             // Values behind the last state, in the last k-step of 16: other sequences', whose
             // infinities and NaN a weight of 0 does not silence
@@ -243,19 +251,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (!ok) break;
-            if (i == 0 || cur.two) {
+            if (i == 0 || cur.info & 0x100u) {
               auto values = [&](int ks) {
                 if (one)
-                  mma_ts(tm + L::kColO + D * i, tm + L::kColP + L::kStepP * i + 8 * ks, b + ks * (2048 >> 4), idesc_o,
+                  mma_ts(tm + L::kColO + D * i, tm + L::kColP + L::kStepP * i + 8 * ks, bv + ks * (2048 >> 4), idesc_o,
                          j > 0 || ks > 0);
               };
-              if (!(ok = warp_wait(bar_p + 16 * i, n_p[i] & 1u, abort))) break;
+              ok = ok && bar_wait(bar_p + 16 * i, ph_p >> i & 1u, abort);
               tm_fence_after();
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                if (ks < steps) values(ks);
-              if (!(ok = warp_wait(bar_p + 16 * i + 8, n_p[i]++ & 1u, abort))) break;
+                if (ok && ks < steps) values(ks);
+              ok = ok && bar_wait(bar_p + 16 * i + 8, ph_p >> i & 1u, abort);
+              ph_p ^= 1u << i;
+              if (!(ok = meet(ok))) break;
               tm_fence_after();
 #pragma unroll
               for (int ks = 4; ks < 8; ++ks)
@@ -269,9 +278,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (ok && one) mma_commit(bar_empty + 8 * vslot);
         }
+        if (!ok || !(cur.info & 0x200u)) break;
         ring += 2 * cur.n;
         cur = next;
-        x = after;
+        j = 0;
       }
       if (!ok) {
         *abort = 1;
