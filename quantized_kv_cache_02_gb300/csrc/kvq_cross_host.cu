@@ -136,20 +136,30 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
   p.n_kv_tokens = c->n_kv_tokens;
   p.status = c->status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int step = tc ? kvq::prompt_tc_tokens(p.g) : kvq::kPromptRows / p.g;
-  for (size_t at = 0; at < seqs.size(); at += kvq::kMaxSeqsPerLaunch) {
-    const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, seqs.size() - at);
-    if (fill_tiles(seqs, at, n, p.Hkv, step, &p.tiles) > kMaxTiles / 4)
-      return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
-  }
-  for (size_t at = 0; at < seqs.size(); at += kvq::kMaxSeqsPerLaunch) {
-    const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, seqs.size() - at);
-    const int64_t tiles = fill_tiles(seqs, at, n, p.Hkv, step, &p.tiles);
-    p.split = tc ? 1 : kvq::prompt_simt_split(tiles, p.tiles.seq[0].kv_len, n_sm);
-    const cudaError_t e = tc ? kvq::launch_cross_tc(p, tiles, n_sm, s)
-                             : kvq::launch_cross_simt(p, c->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
-    if (e != cudaSuccess) return cuda_fail(e, "cross attention launch");
-    kvq::count_launches(1);
+  // sequences of few queries apart from the others
+  const auto many = std::stable_partition(seqs.begin(), seqs.end(), [&](const CrossSeq& x) {
+    return tc && x.q_len <= kvq::cross_few_tokens(p.g);
+  });
+  std::vector<CrossSeq> lists[2] = {{seqs.begin(), many}, {many, seqs.end()}};
+  for (bool launch : {false, true}) {  // every refusal before the first launch
+    for (int k = 0; k < 2; ++k) {
+      std::vector<CrossSeq>& list = lists[k];
+      const bool rows = tc && k == 0;
+      const int step = rows ? kvq::cross_rows_tokens(p.g) : tc ? kvq::prompt_tc_tokens(p.g) : kvq::kPromptRows / p.g;
+      for (size_t at = 0; at < list.size(); at += kvq::kMaxSeqsPerLaunch) {
+        const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, list.size() - at);
+        const int64_t tiles = fill_tiles(list, at, n, p.Hkv, step, &p.tiles);
+        if (tiles > kMaxTiles / 8) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
+        if (!launch) continue;
+        const int32_t most = p.tiles.seq[0].kv_len;
+        p.split = rows ? kvq::cross_rows_split(tiles, most, n_sm) : tc ? 1 : kvq::prompt_simt_split(tiles, most, n_sm);
+        const cudaError_t e = rows ? kvq::launch_cross_rows(p, tiles, s)
+                              : tc ? kvq::launch_cross_tc(p, tiles, n_sm, s)
+                                   : kvq::launch_cross_simt(p, c->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
+        if (e != cudaSuccess) return cuda_fail(e, "cross attention launch");
+        kvq::count_launches(1);
+      }
+    }
   }
   return KVQ_OK;
 }

@@ -192,6 +192,14 @@ cudaError_t launch_weights_tc(const PromptParams& p, int64_t tiles, cudaStream_t
 // prompt_tc_tokens(g) tokens, taken by at most n_sm CTAs
 cudaError_t launch_cross_tc(const CrossParams& p, int64_t tiles, int n_sm, cudaStream_t s);
 
+// the cross attention of few queries (bf16, head_dim 64 or 128): tiles of
+// cross_rows_tokens(g) tokens, a cluster of p.split CTAs each; and up to how many
+// tokens a sequence goes there
+cudaError_t launch_cross_rows(const CrossParams& p, int64_t tiles, cudaStream_t s);
+int cross_rows_tokens(int g);
+int cross_rows_split(int64_t tiles, int32_t max_kv, int n_sm);
+int cross_few_tokens(int g);
+
 // what the tensor cores' rounding takes from a score
 double rounding_loss(double sums);
 
