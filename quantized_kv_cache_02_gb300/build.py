@@ -26,7 +26,7 @@ SOURCES = ["kvq_host.cu", "kvq_append.cu", "kvq_decode_simt.cu", "kvq_decode_mma
            "kvq_decode_mma_b4.cu", "kvq_decode_mma_b8.cu", "kvq_decode_tc.cu", "kvq_restore.cu",
            "kvq_segment.cu", "kvq_prompt_host.cu", "kvq_prompt_simt.cu", "kvq_prompt_tc.cu", "kvq_weights_tc.cu",
            "kvq_evict.cu", "kvq_rotary.cu", "kvq_fork.cu", "kvq_cross_host.cu", "kvq_cross_tc.cu",
-           "kvq_cross_rows.cu"]
+           "kvq_cross_rows.cu", "kvq_cross_few.cu"]
 
 
 def _run(cmd):

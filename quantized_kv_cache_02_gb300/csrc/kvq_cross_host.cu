@@ -137,25 +137,39 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
   p.status = c->status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // sequences of few queries apart from the others
-  const auto many = std::stable_partition(seqs.begin(), seqs.end(), [&](const CrossSeq& x) {
-    return tc && x.q_len <= kvq::cross_few_tokens(p.g);
-  });
-  std::vector<CrossSeq> lists[2] = {{seqs.begin(), many}, {many, seqs.end()}};
+  const int few = tc ? kvq::cross_few_tokens(p.g) : kvq::cross_few_simt_tokens(p.g);
+  const auto many =
+      std::stable_partition(seqs.begin(), seqs.end(), [few](const CrossSeq& x) { return x.q_len <= few; });
+  const int dtype = c->dtype == KVQ_BF16 ? 0 : 1;
+  struct Part {
+    std::vector<CrossSeq> seqs;
+    int step;
+  } parts[2] = {{{seqs.begin(), many}, tc ? kvq::cross_rows_tokens(p.g) : kvq::cross_few_simt_step(p.g)},
+                {{many, seqs.end()}, tc ? kvq::prompt_tc_tokens(p.g) : kvq::kPromptRows / p.g}};
   for (bool launch : {false, true}) {  // every refusal before the first launch
-    for (int k = 0; k < 2; ++k) {
-      std::vector<CrossSeq>& list = lists[k];
-      const bool rows = tc && k == 0;
-      const int step = rows ? kvq::cross_rows_tokens(p.g) : tc ? kvq::prompt_tc_tokens(p.g) : kvq::kPromptRows / p.g;
-      for (size_t at = 0; at < list.size(); at += kvq::kMaxSeqsPerLaunch) {
-        const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, list.size() - at);
-        const int64_t tiles = fill_tiles(list, at, n, p.Hkv, step, &p.tiles);
-        if (tiles > kMaxTiles / 8) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
+    for (Part& part : parts) {
+      for (size_t at = 0; at < part.seqs.size(); at += kvq::kMaxSeqsPerLaunch) {
+        const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, part.seqs.size() - at);
+        const int64_t tiles = fill_tiles(part.seqs, at, n, p.Hkv, part.step, &p.tiles);
+        if (tiles > kMaxTiles / 16) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
         if (!launch) continue;
         const int32_t most = p.tiles.seq[0].kv_len;
-        p.split = rows ? kvq::cross_rows_split(tiles, most, n_sm) : tc ? 1 : kvq::prompt_simt_split(tiles, most, n_sm);
-        const cudaError_t e = rows ? kvq::launch_cross_rows(p, tiles, s)
-                              : tc ? kvq::launch_cross_tc(p, tiles, n_sm, s)
-                                   : kvq::launch_cross_simt(p, c->dtype == KVQ_BF16 ? 0 : 1, tiles, s);
+        cudaError_t e;
+        if (&part == parts && tc) {
+          p.split = kvq::cross_rows_split(tiles, most, n_sm);
+          e = kvq::launch_cross_rows(p, tiles, s);
+        } else if (&part == parts) {
+          int32_t tokens = 0;
+          for (int k = 0; k < n; ++k) tokens = std::max(tokens, p.tiles.seq[k].q_len);
+          p.split = kvq::cross_few_simt_split(tiles, most, n_sm);
+          e = kvq::launch_cross_few_simt(p, dtype, std::min(tokens, part.step) * p.g, tiles, s);
+        } else if (tc) {
+          p.split = kvq::cross_tc_split(d, tiles, most, n_sm);
+          e = kvq::launch_cross_tc(p, tiles, n_sm, s);
+        } else {
+          p.split = kvq::prompt_simt_split(tiles, most, n_sm);
+          e = kvq::launch_cross_simt(p, dtype, tiles, s);
+        }
         if (e != cudaSuccess) return cuda_fail(e, "cross attention launch");
         kvq::count_launches(1);
       }

@@ -19,6 +19,7 @@
 // Bound: HBM, the states read once.  mma.sync and not tcgen05: 16 rows would leave
 // seven eighths of a 128-row accumulator empty, and the copies take longer than these.
 
+#include "kvq_cluster.cuh"
 #include "kvq_prompt.h"
 #include "kvq_tcgen05.cuh"
 
@@ -64,29 +65,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_addr(uint32_t a, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 peer_load4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 peer_load2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-  return v;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kRowsThreads, 2)
     cross_rows_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ RowsMaps maps) {
@@ -284,6 +262,10 @@ cudaError_t launch_rows(const CrossParams& p, const RowsMaps& maps, int64_t tile
   const cudaError_t e = cudaFuncSetAttribute(cross_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)RowsLayout<D>::kSmem);
   if (e != cudaSuccess) return e;
+  if (p.split > 8) {
+    const cudaError_t wide = cudaFuncSetAttribute(cross_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (wide != cudaSuccess) return wide;
+  }
   return launch_cluster(cross_rows_kernel<D>, tiles, p.split, kRowsThreads, RowsLayout<D>::kSmem, s, p, maps);
 }
 
@@ -291,13 +273,17 @@ cudaError_t launch_rows(const CrossParams& p, const RowsMaps& maps, int64_t tile
 
 int cross_rows_tokens(int g) { return 16 / g; }
 
+// One tile: with two, their CTAs read the states twice (8 prompts of 32 rows over 4096
+// states 37 us, the tensor-memory kernel 43; 128 channels; at 64 channels 45 and 35).
 int cross_few_tokens(int g) { return 16 / g; }
 
-// CTAs of a cluster that share a tile: until the SMs are full, each with some runs to stream
+// CTAs of a cluster that share a tile: until the SMs are full, each with some runs to
+// stream.  Clusters of 16 where all of them run at once (8 tiles of 16384 states 24.3 ->
+// 19.2 us); 16 tiles would be 20.8 -> 26 us.
 int cross_rows_split(int64_t tiles, int32_t max_kv, int n_sm) {
   int split = 1;
   while (split < 8 && tiles * split < 2 * (int64_t)n_sm && max_kv >= 2 * split * 8 * kRun) split *= 2;
-  return split;
+  return split == 8 && tiles * 16 <= n_sm && max_kv >= 16 * 8 * kRun ? 16 : split;
 }
 
 cudaError_t launch_cross_rows(const CrossParams& p, int64_t tiles, cudaStream_t s) {

@@ -16,12 +16,16 @@
 // overlap.  The next item's queries and first states are copied while the last
 // blocks run, its first Q K^T follows a tile's last P V at once, and a tile's
 // output leaves (through shared memory of its own) under the other tile's MMAs.
+// Few items of many states are split over a cluster (p.split CTAs, an equal run of
+// blocks each), whose outputs, maxima and sums meet through distributed shared
+// memory, in rank order.
 // Tensor memory, the running maximum that moves only past 2^8, and what is rounded
 // where are as in the causal kernel (kvq_prompt_tc.cu).
 // ("KV Cache 与自回归视频生成", softmax(Q K^T / sqrt(d)) V.)
 
 #include <cfloat>
 
+#include "kvq_cluster.cuh"
 #include "kvq_prompt.h"
 #include "kvq_tcgen05.cuh"
 
@@ -62,6 +66,7 @@ struct Item {
   bool two;            // tile 1 has tokens
 };
 
+template <bool SPLIT>
 __device__ __forceinline__ Item item_at(const CrossParams& p, int x) {
   const Tile t = tile_at(p.tiles, x);
   Item r;
@@ -69,6 +74,12 @@ __device__ __forceinline__ Item item_at(const CrossParams& p, int x) {
   r.head = t.head;
   r.tok0 = t.level * p.tiles.step;
   r.n = (t.seq.kv_len + kKeys - 1) / kKeys;
+  if (SPLIT) {  // this CTA's run of the blocks
+    const int per = (r.n + p.split - 1) / p.split, first = min(r.n, per * (int)(blockIdx.x % p.split));
+    r.n = min(per, r.n - first);
+    r.seq.kv_start += first * kKeys;
+    r.seq.kv_len = min(r.seq.kv_len - first * kKeys, r.n * kKeys);
+  }
   r.two = r.tok0 + p.tiles.step / 2 < t.seq.q_len;
   return r;
 }
@@ -80,7 +91,8 @@ struct Brief {
   uint32_t info;  // states of the last block, tile 1 has tokens (bit 8), another item follows (bit 9)
 };
 
-template <int D>
+// SPLIT: a cluster of p.split CTAs an item, one item a cluster; else items in turn.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ TcMaps maps, int n_items) {
   using L = TcLayout<D>;
@@ -95,6 +107,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   Brief* briefs = reinterpret_cast<Brief*>(smem + L::kBriefs);
   const int tile_tok = p.tiles.step / 2;  // tokens of a tile
+  const int x0 = SPLIT ? blockIdx.x / p.split : blockIdx.x, dx = SPLIT ? n_items : gridDim.x;
 
   if (warp == kMmaWarp) tm_alloc<512>(smem_u32(tslot));
   if (t == 32 * kCopyWarp) {
@@ -131,15 +144,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;
         // the first item with states from x on, or past the end
         auto find = [&](int x, Item* it) {
-          for (; x < n_items; x += gridDim.x) {
-            *it = item_at(p, x);
+          for (; x < n_items; x += dx) {
+            *it = item_at<SPLIT>(p, x);
             if (it->n > 0) break;
           }
           return x;
         };
         Item it, next;
-        for (int x = find(blockIdx.x, &it), after, k = 0; x < n_items && ok; x = after, it = next, ++k) {
-          after = find(x + gridDim.x, &next);
+        for (int x = find(x0, &it), after, k = 0; x < n_items && ok; x = after, it = next, ++k) {
+          after = find(x + dx, &next);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!ok || (i == 1 && !it.two)) break;
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = true;
       // Block -1 stands for the end of an item before the first (items come by falling
       // number of states).
-      Brief cur = {0, item_at(p, blockIdx.x).n > 0 ? 0x200u : 0u}, next = {};
+      Brief cur = {0, item_at<SPLIT>(p, x0).n > 0 ? 0x200u : 0u}, next = {};
       int j = -1, begun = 0;
       for (;;) {
         const int rest = cur.info & 0xff;
@@ -295,6 +308,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
     }
+    if constexpr (SPLIT) {  // (the softmax warps join the outputs in between)
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ============ softmax: tile i, one row a thread ===================================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -305,13 +322,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                    tp = tm + L::kColP + L::kStepP * i + lanes;
     const float2 sc = make_float2(p.scale2, p.scale2);
     uint8_t* stage = smem + L::kStage + warp * L::kStageWarp;
+    float2* ml = reinterpret_cast<float2*>(smem + L::kStage);  // (split: of every row, in place of the stage)
     uint32_t n_s = 0, n_o = 0;
     bool ok = true;
-    for (int x = blockIdx.x; x < n_items && ok; x += gridDim.x) {
+    for (int x = x0; x < n_items && ok; x += dx) {
       int n, kv_len;
       bool warp_live;
       {
-        const Item it = item_at(p, x);
+        const Item it = item_at<SPLIT>(p, x);
         if (i == 1 && !it.two) continue;
         n = it.n;
         kv_len = it.seq.kv_len;
@@ -399,7 +417,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!ok) break;
       if (!warp_live) continue;
       tm_fence_after();
-      const Item it = item_at(p, x);  // (again: kept over the blocks it would cost them registers)
+      if constexpr (SPLIT) {
+        ml[t] = make_float2(m, l);
+        continue;
+      }
+      const Item it = item_at<SPLIT>(p, x);  // (again: kept over the blocks it would cost them registers)
       const int pos = it.tok0 + i * tile_tok + tt, head = it.head * p.g + member;
       const bool live = tt < tile_tok && pos < it.seq.q_len;
       const float inv = 1.f / l;
@@ -442,6 +464,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       *abort = 1;
       if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
     }
+    if constexpr (SPLIT) {
+      // Both tiles' MMAs are done: the ring takes the outputs, D floats a row, 16-byte
+      // pieces swizzled by row.
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const Item it = item_at<SPLIT>(p, x0);
+      const int rank = blockIdx.x % p.split, rows = min(2 * tile_tok, it.seq.q_len - it.tok0);
+      constexpr int kPieces = D / 4;
+      float* part = reinterpret_cast<float*>(smem + L::kRing);
+      if (__any_sync(0xffffffffu, tt < tile_tok && i * tile_tok + tt < rows)) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tm_ld32(to + 32 * c, o);
+          tm_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + t * D + 4 * ((8 * c + e / 4) ^ (t & (kPieces - 1)))) =
+                it.n > 0 ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        tm_fence_before();
+      }
+      cluster_sync();
+      const int kv_len = tile_at(p.tiles, x0).seq.kv_len;  // all ranks'
+      for (int y = rank * 256 + t; y < rows * p.g * kPieces; y += p.split * 256) {
+        const int live_row = y / kPieces, c = y % kPieces;
+        const int token = live_row / p.g, at_tile = token / tile_tok;
+        const int row = 128 * at_tile + live_row - at_tile * tile_tok * p.g;  // (a tile's last rows may be idle)
+        const uint32_t at_ml = sbase + L::kStage + row * 8,
+                       at_o = sbase + L::kRing + (row * D + 4 * (c ^ (row & (kPieces - 1)))) * 4;
+        float top = -FLT_MAX;
+        for (int k = 0; k < p.split; ++k) top = fmaxf(top, peer_load2(peer_addr(at_ml, k)).x);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lr = 0.f;
+        for (int k = 0; k < p.split; ++k) {
+          const float2 part_ml = peer_load2(peer_addr(at_ml, k));
+          const float4 v = peer_load4(peer_addr(at_o, k));
+          const float a = ex2(part_ml.x - top);
+          lr = fmaf(part_ml.y, a, lr);
+          sum.x = fmaf(v.x, a, sum.x);
+          sum.y = fmaf(v.y, a, sum.y);
+          sum.z = fmaf(v.z, a, sum.z);
+          sum.w = fmaf(v.w, a, sum.w);
+        }
+        const float inv = kv_len == 0 ? 0.f : 1.f / lr;  // over no states: zeros, and lse minus infinity
+        const int64_t pos = it.seq.q_start + it.tok0 + token;
+        const int head = it.head * p.g + live_row - token * p.g;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + pos * p.o_ts + (int64_t)head * p.o_hs + 4 * c) =
+            make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+        if (p.lse && c == 0)
+          p.lse[(int64_t)head * p.n_tokens + pos] =
+              kv_len == 0 ? -INFINITY : (top + log2f(lr)) * 0.69314718055994530942f;
+      }
+      cluster_sync();  // no CTA ends while another reads its outputs
+    }
   }
   tm_fence_before();
   __syncthreads();
@@ -452,16 +528,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool SPLIT>
 cudaError_t launch_tc(const CrossParams& p, const TcMaps& maps, int64_t tiles, int n_sm, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)TcLayout<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cross_tc_kernel<D>, dim3((unsigned)(tiles < n_sm ? tiles : n_sm)), dim3(kTcThreads),
-                    TcLayout<D>::kSmem, s, p, maps, (int)tiles);
+  return launch_cluster(cross_tc_kernel<D, SPLIT>, SPLIT || tiles < n_sm ? tiles : n_sm, p.split, kTcThreads,
+                        TcLayout<D>::kSmem, s, p, maps, (int)tiles);
+}
+
+template <int D>
+int split_of(int64_t tiles, int32_t max_kv, int n_sm) {
+  if (cudaFuncSetAttribute(cross_tc_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)TcLayout<D>::kSmem) != cudaSuccess)
+    return 1;
+  const int64_t blocks = (max_kv + kKeys - 1) / kKeys;
+  for (int split = 8; split > 1; --split)
+    if (tiles * split <= n_sm && blocks >= 2 * split &&
+        tiles <= active_clusters<cross_tc_kernel<D, true>>(split, kTcThreads, TcLayout<D>::kSmem))
+      return split;
+  return 1;
 }
 
 }  // namespace
+
+// CTAs of a cluster that share an item's blocks: while all clusters run at once, each
+// CTA with two blocks or more (256 rows over 16384 states: 150 us with one, 27 with 8).
+int cross_tc_split(int d, int64_t tiles, int32_t max_kv, int n_sm) {
+  return d == 128 ? split_of<128>(tiles, max_kv, n_sm) : split_of<64>(tiles, max_kv, n_sm);
+}
 
 cudaError_t launch_cross_tc(const CrossParams& p, int64_t tiles, int n_sm, cudaStream_t s) {
   TcMaps maps;
@@ -470,7 +565,9 @@ cudaError_t launch_cross_tc(const CrossParams& p, int64_t tiles, int n_sm, cudaS
       !tma_map3(&maps.k, p.k, p.D, p.n_kv_tokens, p.Hkv, p.k_ts, p.k_hs, kKeys, 1) ||
       !tma_map3(&maps.v, p.v, p.D, p.n_kv_tokens, p.Hkv, p.v_ts, p.v_hs, kKeys, 1))
     return cudaErrorInvalidValue;
-  return p.D == 128 ? launch_tc<128>(p, maps, tiles, n_sm, s) : launch_tc<64>(p, maps, tiles, n_sm, s);
+  if (p.split > 1)
+    return p.D == 128 ? launch_tc<128, true>(p, maps, tiles, n_sm, s) : launch_tc<64, true>(p, maps, tiles, n_sm, s);
+  return p.D == 128 ? launch_tc<128, false>(p, maps, tiles, n_sm, s) : launch_tc<64, false>(p, maps, tiles, n_sm, s);
 }
 
 }  // namespace kvq

@@ -5,6 +5,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -169,6 +171,33 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int64_t tiles, int split, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Clusters of ``size`` CTAs of a kernel that run at once on the current device, asked
+// for once a size; 0 if unknown.
+template <auto KERNEL>
+int active_clusters(int size, int threads, size_t smem) {
+  static std::atomic<int> known[64][17];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || size > 16) return 0;
+  int n = known[dev][size].load();
+  if (n) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev][size].store(n + 1);
+  return n;
+}
+
 // Launchers (return the launch's error code).
 cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
 cudaError_t launch_cross_simt(const CrossParams& p, int dtype, int64_t tiles, cudaStream_t s);
@@ -189,7 +218,8 @@ void weights_tc_plan(int64_t pairs, int64_t most_tokens, int g, int n_sm, int* c
 cudaError_t launch_weights_tc(const PromptParams& p, int64_t tiles, cudaStream_t s);
 
 // the tensor-core cross attention (bf16, head_dim 64 or 128): tiles of
-// prompt_tc_tokens(g) tokens, taken by at most n_sm CTAs
+// prompt_tc_tokens(g) tokens, taken by at most n_sm CTAs or each by a cluster of p.split
+int cross_tc_split(int d, int64_t tiles, int32_t max_kv, int n_sm);
 cudaError_t launch_cross_tc(const CrossParams& p, int64_t tiles, int n_sm, cudaStream_t s);
 
 // the cross attention of few queries (bf16, head_dim 64 or 128): tiles of
@@ -199,6 +229,12 @@ cudaError_t launch_cross_rows(const CrossParams& p, int64_t tiles, cudaStream_t 
 int cross_rows_tokens(int g);
 int cross_rows_split(int64_t tiles, int32_t max_kv, int n_sm);
 int cross_few_tokens(int g);
+
+// the same on CUDA cores: tiles of cross_few_simt_step(g) tokens, at most ``rows`` rows each
+cudaError_t launch_cross_few_simt(const CrossParams& p, int dtype, int rows, int64_t tiles, cudaStream_t s);
+int cross_few_simt_step(int g);
+int cross_few_simt_tokens(int g);
+int cross_few_simt_split(int64_t tiles, int32_t max_kv, int n_sm);
 
 // what the tensor cores' rounding takes from a score
 double rounding_loss(double sums);

@@ -204,3 +204,32 @@ def test_no_work_and_refusals(torch, kvq):
             kvq.cross_attention(q, k, v, *args)
     with pytest.raises(TypeError):
         kvq.cross_attention(q, k, v, [8], [1.5])
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 2, 64, "bfloat16"), (7, 1, 128, "bfloat16"), (2, 2, 128, "bfloat16"),
+                                            (5, 1, 64, "bfloat16"), (4, 2, 128, "float32"), (3, 1, 80, "bfloat16")])
+@pytest.mark.parametrize("q_lens,kv_lens", [
+    ([1], [5000]), ([2, 1, 1], [1027, 0, 2500]), ([100], [5000]), ([33, 1, 70], [1500, 2000, 130]),
+    ([40, 50, 60], [0, 3000, 129]), ([64], [1025]), ([300, 2], [700, 4100]), ([129], [2049])])
+def test_split_states(torch, kvq, hq, hkv, d, dtype, q_lens, kv_lens):
+    """Few tiles over many states: clusters of CTAs, some without states, join their results."""
+    q, k, v = inputs(torch, sum(q_lens) + 1, sum(kv_lens) + 5, hq, hkv, d, dtype, 9)
+    out, lse = torch.full_like(q, 7.0), torch.full((hq, len(q)), 7.0, device="cuda")
+    k[sum(kv_lens):], v[sum(kv_lens):] = math.nan, math.inf
+    kvq.cross_attention(q, k, v, q_lens, kv_lens, out=out, lse=lse)
+    check(torch, out, lse, q, k, v, q_lens, kv_lens)
+    assert (out[sum(q_lens):] == 7.0).all() and (lse[:, sum(q_lens):] == 7.0).all()
+    again, lse2 = kvq.cross_attention(q, k, v, q_lens, kv_lens)
+    assert torch.equal(again[:-1], out[:-1]) and torch.equal(lse2[:, :-1], lse[:, :-1]) and kvq.prompt_status() == 0
+
+
+def test_split_states_minus_infinity(torch, kvq):
+    """Ranks that see only scores of minus infinity weigh nothing."""
+    for n in (1, 90):
+        q, k, v = inputs(torch, n, 3000, 2, 2, 128, "bfloat16", 4)
+        q = q.abs() + 0.5
+        k[:2900] = -math.inf
+        out, lse = kvq.cross_attention(q, k, v, [n], [3000])
+        check(torch, out, lse, q, k[2900:], v[2900:], [n], [100])
+        out, lse = kvq.cross_attention(q, k, v, [n], [2900])
+        assert out.isnan().all() and (lse == -math.inf).all()
