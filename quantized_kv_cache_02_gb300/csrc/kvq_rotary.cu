@@ -10,10 +10,12 @@
 // upper 32 bits are split into a quadrant and an eighth of a turn to either side
 // of it, where sincospif keeps the fp32 step of small arguments.
 //
-// Bound: HBM, each element read and written once.  A thread takes one 16-byte
-// piece (or the two that hold the halves of its pairs) of one token, computes its
-// sines once and walks a run of the q and then of the k heads, the next heads'
-// loads in flight while it turns the last.
+// Bound: HBM, each element read and written once.  A block takes a few tokens with all
+// their q and k heads, so each angle is computed once (its table entry is a
+// divergent constant load and its sine and cosine some 60 instructions: computed by
+// every thread for its own pieces they took as long as the copies).  A thread keeps a
+// 16-byte piece's place (or the two that hold the halves of its pairs) and its sines
+// through a run of heads, the next heads' loads in flight while it turns the last.
 // ("KV Cache 与自回归视频生成": the cache holds Keys after their positions.)
 
 #include <cuda_bf16.h>
@@ -29,8 +31,11 @@ namespace kvq {
 namespace {
 
 constexpr int kMaxPairs = 128, kMaxAxes = 4;
-constexpr int kRotaryThreads = 256;
+constexpr int kRotaryThreads = 256, kMaxAngles = 2048;
 constexpr int kAhead = 4;  // heads loaded at once
+// Blocks an SM below which a block takes fewer tokens (14400 tokens of 32 + 8 heads of 128 in
+// us: 4 48.8, 6 46.4, 16 51.5, 32 63.7; 4096 tokens: 14.0, 14.0, 21.2, 21.3).
+constexpr int kBlocksPerSm = 6;
 
 struct RotaryTensor {
   const void* in;
@@ -42,7 +47,8 @@ struct RotaryTensor {
 struct RotaryParams {
   int32_t D, pairs, items, n_tensors;
   int32_t heads;               // of all tensors
-  int32_t run;                 // heads a thread takes
+  int32_t tokens, lanes;       // of a block: tokens, and heads taken side by side
+  int32_t run;                 // heads a block takes
   int32_t inverse, wide;       // wide: 8-byte positions
   int64_t n_tokens;
   const void* positions;
@@ -63,25 +69,19 @@ __device__ __forceinline__ void sincos_turns(uint64_t turns, float* c, float* s)
   *s = (quadrant & 2u) ? -ss : ss;
 }
 
-// A thread's share of a head: one 16-byte piece of E elements at A (and one at B), or single elements.
-enum Shape { kHalves, kAdjacent, kSingle };
+// A thread's share of a head: one 16-byte piece of E elements at A (and, for halves, one at B).
+enum Shape { kHalves, kAdjacent, kRows };
 
 template <typename T, int SHAPE>
 struct Share {
-  static constexpr int E = SHAPE == kSingle ? 1 : 16 / (int)sizeof(T);
+  static constexpr int E = 16 / (int)sizeof(T);
   static constexpr int kAngles = SHAPE == kAdjacent ? E / 2 : E;
   T a[E], b[SHAPE == kAdjacent ? 1 : E];
 };
 
-template <int E, typename T>
-__device__ __forceinline__ void load_piece(T* dst, const T* src) {
-  if constexpr (E == 1) *dst = *src;
-  else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-}
-template <int E, typename T>
-__device__ __forceinline__ void store_piece(T* dst, const T* src) {
-  if constexpr (E == 1) *dst = *src;
-  else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+template <typename T>
+__device__ __forceinline__ void move_piece(T* dst, const T* src) {
+  *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
 }
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -91,15 +91,51 @@ __device__ __forceinline__ T from_float(float x) {
   else return x;
 }
 
+// [token][pair]: cosine and sine.  A warp's lanes lie along the tokens, so that few of its
+// table entries differ.
+__device__ __forceinline__ void fill_angles(const RotaryParams& p, int64_t first, int n_tok, float2* turned) {
+  for (int y = threadIdx.x; y < n_tok * p.pairs; y += kRotaryThreads) {
+    const int pair = y / n_tok, t = y - pair * n_tok;
+    const int64_t at = (first + t) * p.p_ts + p.axis[pair] * p.p_as;
+    const int64_t pos = p.wide ? static_cast<const int64_t*>(p.positions)[at]
+                               : (int64_t)static_cast<const int32_t*>(p.positions)[at];
+    float2 cs;
+    sincos_turns((uint64_t)pos * p.turns[pair], &cs.x, &cs.y);
+    if (p.inverse) cs.y = -cs.y;
+    turned[t * p.pairs + pair] = cs;
+  }
+}
+
+// Head ``head`` of all tensors' heads, of a token.
+template <typename T>
+__device__ __forceinline__ const T* head_in(const RotaryParams& p, int64_t token, int head) {
+  const RotaryTensor& t = p.t[head >= p.t[0].heads];
+  return static_cast<const T*>(t.in) + token * t.in_ts + (head - (head >= p.t[0].heads ? p.t[0].heads : 0)) * t.in_hs;
+}
+template <typename T>
+__device__ __forceinline__ T* head_out(const RotaryParams& p, int64_t token, int head) {
+  const RotaryTensor& t = p.t[head >= p.t[0].heads];
+  return static_cast<T*>(t.out) + token * t.out_ts + (head - (head >= p.t[0].heads ? p.t[0].heads : 0)) * t.out_hs;
+}
+
+// x1, x2 by the angle of cs, rounded once.
+template <typename T>
+__device__ __forceinline__ void turn(T& u, T& v, float2 cs) {
+  const float x1 = to_float(u), x2 = to_float(v);
+  u = from_float<T>(fmaf(x1, cs.x, -x2 * cs.y));
+  v = from_float<T>(fmaf(x1, cs.y, x2 * cs.x));
+}
+
 template <typename T, int SHAPE>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using S = Share<T, SHAPE>;
-  const int64_t idx = (int64_t)blockIdx.x * kRotaryThreads + threadIdx.x;
-  const int64_t token = idx / p.items;
-  const int item = (int)(idx - token * p.items);
+  __shared__ __align__(16) float2 turned[kMaxAngles];  // [token][pair]: cosine, sine
+  const int tid = threadIdx.x, slot = tid / p.items, item = tid - slot * p.items;
+  const int lane = slot / p.tokens, own = slot - lane * p.tokens;
+  const int64_t first = (int64_t)blockIdx.x * p.tokens, token = first + own;
+  const int n_tok = (int)min((int64_t)p.tokens, p.n_tokens - first);
   pdl_wait();
   pdl_release();
-  if (token >= p.n_tokens) return;
 
   // where the share lies, its pairs, and whether it only passes through
   int at_a, at_b = 0, pair0;
@@ -109,73 +145,100 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     pair0 = at_a / 2;
     through = pair0 >= p.pairs;
   } else {
-    const int turned = p.pairs / S::E;
-    through = item >= turned;
-    at_a = through ? 2 * p.pairs + (item - turned) * S::E : item * S::E;
+    const int pieces = p.pairs / S::E;
+    through = item >= pieces;
+    at_a = through ? 2 * p.pairs + (item - pieces) * S::E : item * S::E;
     at_b = at_a + p.pairs;
     pair0 = at_a;
   }
-  const int h0 = blockIdx.y * p.run, h1 = min(p.heads, h0 + p.run);
+  const int h1 = min(p.heads, (int)(blockIdx.y + 1) * p.run);
+  int h = lane < p.lanes && own < n_tok ? blockIdx.y * p.run + lane : h1;  // (threads past the last lane have no work)
 
-  float c[S::kAngles], s[S::kAngles];
-  bool ready = false;
-  auto angles = [&] {
-    ready = true;
-    if (through) return;
-    const int64_t row = token * p.p_ts;
+  S x[kAhead];
+  auto load = [&] {
 #pragma unroll
-    for (int i = 0; i < S::kAngles; ++i) {
-      const int pair = pair0 + i;
-      if (SHAPE == kAdjacent && pair >= p.pairs) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-        continue;
-      }
-      const int64_t at = row + p.axis[pair] * p.p_as;
-      const int64_t pos = p.wide ? static_cast<const int64_t*>(p.positions)[at]
-                                 : (int64_t)static_cast<const int32_t*>(p.positions)[at];
-      sincos_turns((uint64_t)pos * p.turns[pair], &c[i], &s[i]);
-      if (p.inverse) s[i] = -s[i];
+    for (int e = 0; e < kAhead; ++e) {
+      if (h + e * p.lanes >= h1) break;
+      const T* in = head_in<T>(p, token, h + e * p.lanes);
+      move_piece(x[e].a, in + at_a);
+      if (SHAPE != kAdjacent && !through) move_piece(x[e].b, in + at_b);
     }
   };
-  auto turn = [&](S& x) {
-    if (through) return;
+  load();
+  fill_angles(p, first, n_tok, turned);  // under the first loads
+  __syncthreads();
+  if (h >= h1) return;
+  float2 cs[S::kAngles];
 #pragma unroll
-    for (int i = 0; i < S::kAngles; ++i) {
-      T& u = SHAPE == kAdjacent ? x.a[2 * i] : x.a[i];
-      T& v = SHAPE == kAdjacent ? x.a[2 * i + 1] : x.b[i];
-      if (SHAPE == kAdjacent && pair0 + i >= p.pairs) continue;  // as it is, infinities too
-      const float x1 = to_float(u), x2 = to_float(v);
-      u = from_float<T>(fmaf(x1, c[i], -x2 * s[i]));
-      v = from_float<T>(fmaf(x1, s[i], x2 * c[i]));
+  for (int i = 0; i < S::kAngles; ++i) {
+    const bool real = !through && pair0 + i < p.pairs;
+    cs[i] = real ? turned[own * p.pairs + pair0 + i] : make_float2(1.f, 0.f);
+  }
+  while (true) {
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      if (h + e * p.lanes >= h1) break;
+      if (!through) {
+#pragma unroll
+        for (int i = 0; i < S::kAngles; ++i) {
+          T& u = SHAPE == kAdjacent ? x[e].a[2 * i] : x[e].a[i];
+          T& v = SHAPE == kAdjacent ? x[e].a[2 * i + 1] : x[e].b[i];
+          if (SHAPE == kAdjacent && pair0 + i >= p.pairs) continue;  // as it is, infinities too
+          turn(u, v, cs[i]);
+        }
+      }
+      T* out = head_out<T>(p, token, h + e * p.lanes);
+      move_piece(out + at_a, x[e].a);
+      if (SHAPE != kAdjacent && !through) move_piece(out + at_b, x[e].b);
     }
-  };
+    h += kAhead * p.lanes;
+    if (h >= h1) break;
+    load();
+  }
+}
 
-  int before = 0;
-  for (int n = 0; n < p.n_tensors; ++n) {
-    const RotaryTensor& t = p.t[n];
-    const int first = max(h0 - before, 0), last = min(h1 - before, t.heads);
-    before += t.heads;
-    const T* in = static_cast<const T*>(t.in) + token * t.in_ts;
-    T* out = static_cast<T*>(t.out) + token * t.out_ts;
-    if (first >= last || (through && in == out)) continue;
-    S x[kAhead];
-    for (int h = first; h < last; h += kAhead) {
+// Halves whose second one starts off a 16-byte step: a warp takes whole heads through
+// shared memory, 2 KB at a time, and turns them there.
+template <typename T>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_rows_kernel(const __grid_constant__ RotaryParams p) {
+  constexpr int kPieces = 32 * kAhead, kE = 16 / (int)sizeof(T);
+  __shared__ __align__(16) float2 turned[kMaxAngles];
+  __shared__ uint4 pieces[kRotaryThreads / 32][kPieces];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = (int64_t)blockIdx.x * p.tokens;
+  const int n_tok = (int)min((int64_t)p.tokens, p.n_tokens - first);
+  pdl_wait();
+  pdl_release();
+  fill_angles(p, first, n_tok, turned);
+  __syncthreads();
+  const int per_head = p.D / kE, at_once = kPieces / per_head;  // heads in the warp's pieces
+  const int h0 = blockIdx.y * p.run, heads = min(p.heads - h0, p.run), all = n_tok * heads;
+  uint4* mine = pieces[warp];
+  for (int r0 = warp * at_once; r0 < all; r0 += kRotaryThreads / 32 * at_once) {
+    const int n = min(at_once, all - r0);
+    uint4 x[kAhead];
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        if (h + e >= last) break;
-        load_piece<S::E>(x[e].a, in + (h + e) * t.in_hs + at_a);
-        if (SHAPE != kAdjacent && !through) load_piece<S::E>(x[e].b, in + (h + e) * t.in_hs + at_b);
-      }
-      if (!ready) angles();  // under the first loads
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        if (h + e >= last) break;
-        turn(x[e]);
-        store_piece<S::E>(out + (h + e) * t.out_hs + at_a, x[e].a);
-        if (SHAPE != kAdjacent && !through) store_piece<S::E>(out + (h + e) * t.out_hs + at_b, x[e].b);
-      }
+    for (int e = 0; e < kAhead; ++e) {
+      const int y = lane + 32 * e, r = y / per_head, t = (r0 + r) / heads;
+      if (r < n)
+        x[e] = reinterpret_cast<const uint4*>(head_in<T>(p, first + t, h0 + r0 + r - t * heads))[y - r * per_head];
     }
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) mine[lane + 32 * e] = x[e];  // (past the heads: not looked at)
+    __syncwarp();
+    for (int y = lane; y < n * p.pairs; y += 32) {
+      const int r = y / p.pairs, pair = y - r * p.pairs, t = (r0 + r) / heads;
+      T* row = reinterpret_cast<T*>(mine) + r * p.D;
+      turn(row[pair], row[pair + p.pairs], turned[t * p.pairs + pair]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int y = lane + 32 * e, r = y / per_head, t = (r0 + r) / heads;
+      if (r < n)
+        reinterpret_cast<uint4*>(head_out<T>(p, first + t, h0 + r0 + r - t * heads))[y - r * per_head] = mine[y];
+    }
+    __syncwarp();
   }
 }
 
@@ -184,7 +247,7 @@ cudaError_t launch_t(const RotaryParams& p, Shape shape, dim3 grid, cudaStream_t
   const dim3 block(kRotaryThreads);
   return shape == kHalves     ? launch_pdl(rotary_kernel<T, kHalves>, grid, block, 0, s, p)
          : shape == kAdjacent ? launch_pdl(rotary_kernel<T, kAdjacent>, grid, block, 0, s, p)
-                              : launch_pdl(rotary_kernel<T, kSingle>, grid, block, 0, s, p);
+                              : launch_pdl(rotary_rows_kernel<T>, grid, block, 0, s, p);
 }
 
 // f / 2 pi modulo 1 in units of 2^-64: the quotient in two doubles (its product
@@ -265,16 +328,20 @@ kvq_status rotary(const kvq_rotary_plan* plan, const void* positions, int32_t po
   p.positions = positions;
   p.p_ts = position_token_stride;
   p.p_as = position_axis_stride;
-  // halves whose second one starts off a 16-byte step go element by element
   const int piece = 16 / es;
-  const Shape shape = plan->interleaved ? kAdjacent : p.pairs % piece == 0 ? kHalves : kSingle;
-  p.items = shape == kAdjacent ? d / piece : shape == kHalves ? d / piece - p.pairs / piece : d - p.pairs;
+  const Shape shape = plan->interleaved ? kAdjacent : p.pairs % piece == 0 ? kHalves : kRows;
+  p.items = shape == kHalves ? d / piece - p.pairs / piece : d / piece;
   int n_sm = 0;
   KVQ_TRY(sm_count(&n_sm));
-  const int64_t threads = n_tokens * p.items, blocks = (threads + kRotaryThreads - 1) / kRotaryThreads;
+  // As many tokens a block as leave enough blocks (and its threads fit), then the heads
+  // side by side; with few tokens the heads are split among blocks too.
+  p.tokens = 1;
+  while (2 * p.tokens * p.items <= kRotaryThreads && 2 * p.tokens * p.pairs <= kMaxAngles && n_tokens >= 2 * p.tokens * kBlocksPerSm * (int64_t)n_sm) p.tokens *= 2;
+  p.lanes = std::min(p.heads, kRotaryThreads / (p.tokens * p.items));
+  const int64_t blocks = (n_tokens + p.tokens - 1) / p.tokens;
   if (blocks > kMaxTiles) return fail(KVQ_EUNSUPPORTED, "too many tokens for one launch");
   p.run = p.heads;
-  while (p.run > 1 && blocks * ((p.heads + p.run - 1) / p.run) < 8 * (int64_t)n_sm) p.run = (p.run + 1) / 2;
+  while (p.run > p.lanes && blocks * ((p.heads + p.run - 1) / p.run) < 2 * (int64_t)n_sm) p.run = (p.run + 1) / 2;
   p.run = std::max(p.run, (p.heads + 65534) / 65535);
   const dim3 grid((unsigned)blocks, (unsigned)((p.heads + p.run - 1) / p.run));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
