@@ -167,7 +167,7 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
           p.split = kvq::cross_tc_split(d, tiles, most, n_sm);
           e = kvq::launch_cross_tc(p, tiles, n_sm, s);
         } else {
-          p.split = kvq::prompt_simt_split(tiles, most, n_sm);
+          p.split = kvq::cross_simt_split(tiles, most, n_sm);
           e = kvq::launch_cross_simt(p, dtype, tiles, s);
         }
         if (e != cudaSuccess) return cuda_fail(e, "cross attention launch");

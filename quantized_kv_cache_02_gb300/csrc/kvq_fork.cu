@@ -11,6 +11,8 @@
 // sequence, and the host orders the steps so that each sequence is read before it is
 // written; of a cycle one sequence's columns wait in registers.
 
+#include <algorithm>
+
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -20,8 +22,8 @@ struct alignas(16) Quad {
   uint32_t w[4];
 };
 
-template <typename V>
-__device__ __forceinline__ void copy_columns(const ForkParams& p, const ForkRegion& r, int unit, int64_t col0) {
+template <typename V, int N>
+__device__ __forceinline__ void copy_columns(const ForkParams<N>& p, const ForkRegion& r, int unit, int64_t col0) {
   V v[kForkDepth], held[kForkDepth];
   bool held_live[kForkDepth] = {};
   auto place = [&](int seq) {
@@ -68,7 +70,8 @@ __device__ __forceinline__ void copy_columns(const ForkParams& p, const ForkRegi
   }
 }
 
-__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkParams p) {
+template <int N>
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkParams<N> p) {
   int n = 0;
   while (n + 1 < p.n_regions && p.region[n + 1].first_block <= blockIdx.x) ++n;
   const ForkRegion& r = p.region[n];
@@ -78,14 +81,25 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
   const int64_t col0 = (at - unit * per_unit) * kForkCols + threadIdx.x;
   pdl_wait();
   pdl_release();
-  if (r.grain == 16) copy_columns<Quad>(p, r, unit, col0);
-  else copy_columns<uint32_t>(p, r, unit, col0);
+  if (r.grain == 16) copy_columns<Quad, N>(p, r, unit, col0);
+  else copy_columns<uint32_t, N>(p, r, unit, col0);
 }
 
 }  // namespace
 
-cudaError_t launch_fork(const ForkParams& p, int64_t blocks, int components, cudaStream_t s) {
-  return launch_pdl(fork_kernel, dim3((unsigned)blocks, (unsigned)components), dim3(kForkThreads), 0, s, p);
+cudaError_t launch_fork(const ForkParams<kMaxForkSteps>& p, int steps, int copies, int64_t blocks, int components,
+                        cudaStream_t s) {
+  const dim3 grid((unsigned)blocks, (unsigned)components), block(kForkThreads);
+  if (steps > kFewForkSteps || copies > kFewForkSteps) return launch_pdl(fork_kernel<kMaxForkSteps>, grid, block, 0, s, p);
+  ForkParams<kFewForkSteps> few;
+  few.n_regions = p.n_regions;
+  few.rcap = p.rcap;
+  few.layout = p.layout;
+  std::copy(p.region, p.region + p.n_regions, few.region);
+  std::copy(p.component, p.component + components + 1, few.component);
+  std::copy(p.step, p.step + steps, few.step);
+  std::copy(p.dst, p.dst + copies, few.dst);
+  return launch_pdl(fork_kernel<kFewForkSteps>, grid, block, 0, s, few);
 }
 
 }  // namespace kvq

@@ -1251,8 +1251,8 @@ kvq_status fork_impl(kvq_cache* c, const int32_t* src, const int32_t* dst, int32
       return fail(KVQ_EUNSUPPORTED, "more than %d sequences depend on one another in one call", kvq::kMaxForkSteps);
   }
   const int64_t H = c->cfg.n_kv_heads, D = c->cfg.head_dim;
-  kvq::ForkParams p;
-  memset(&p, 0, sizeof p);
+  kvq::ForkParams<kvq::kMaxForkSteps> p;
+  p.n_regions = 0;
   p.rcap = c->rcap;
   p.layout = c->layout;
   int64_t most_q = 0;
@@ -1317,7 +1317,7 @@ kvq_status fork_impl(kvq_cache* c, const int32_t* src, const int32_t* dst, int32
       }
     }
     p.component[components] = steps;
-    const cudaError_t e = kvq::launch_fork(p, blocks, components, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = kvq::launch_fork(p, steps, copies, blocks, components, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "fork launch");
     g_launches += 1;
   }
@@ -1553,6 +1553,7 @@ kvq_status kvq_restore(const kvq_cache* c, int32_t seq_begin, int32_t n_seqs, vo
     p.v_out = static_cast<uint8_t*>(v_out) + off;
     p.t_stride = t_stride;
     p.page_cols = (int)pmax;
+    p.n_sm = c->n_sm;
     p.seq_begin = s0;
     p.n_seqs = n;
     fill_counters(c, s0, n, p.ctr);

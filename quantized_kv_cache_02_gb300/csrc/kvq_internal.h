@@ -253,7 +253,9 @@ struct RestoreParams {
   int64_t t_stride;
   SegArrays seg;               // segmented caches
   int32_t page_cols;           // pages of the longest unit (the launcher turns it into
-                               // columns of page runs; the window column follows)
+                               // columns of page runs; the window columns follow)
+  int32_t run;                 // pages of a run (set by the launcher)
+  int32_t n_sm;
   int32_t seq_begin, n_seqs;
   SeqCounters ctr[kMaxSeqsPerLaunch];
 };
@@ -285,15 +287,18 @@ struct ForkStep {
 
 // Columns a fork block copies (every thread several at once).
 constexpr int kForkThreads = 128, kForkDepth = 4, kForkCols = kForkThreads * kForkDepth;
-constexpr int kMaxForkSteps = 512, kMaxForkRegions = 8;
+constexpr int kFewForkSteps = 16, kMaxForkSteps = 512, kMaxForkRegions = 8;
 
+// N: the steps and copies that fit.  (A launch pays for its parameters: with 18 KB of them
+// a small fork's call took 2 us longer than with 2.)
+template <int N>
 struct ForkParams {
   int32_t n_regions, rcap;
   const SeqLayout* layout;
   ForkRegion region[kMaxForkRegions];
-  int32_t component[kMaxForkSteps + 1];  // first step of each (blockIdx.y), and the end
-  ForkStep step[kMaxForkSteps];
-  int32_t dst[kMaxForkSteps];
+  int32_t component[N + 1];         // first step of each (blockIdx.y), and the end
+  ForkStep step[N];
+  int32_t dst[N];
 };
 
 // The datawhale page's compare: quantize a Key/Value pair, restore, sum the
@@ -338,7 +343,9 @@ bool decode_tc_supported(const DecodeParams& p);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t s);
 cudaError_t launch_decode_dense(const DecodeParams& p, cudaStream_t s, int* supported);
 cudaError_t launch_restore(const RestoreParams& p, cudaStream_t s);
-cudaError_t launch_fork(const ForkParams& p, int64_t blocks, int components, cudaStream_t s);
+// of the first ``steps`` steps; with few of them only those are passed on
+cudaError_t launch_fork(const ForkParams<kMaxForkSteps>& p, int steps, int copies, int64_t blocks, int components,
+                        cudaStream_t s);
 // segmented caches: pass 1 (Key absmax, Value codes), pass 2 (Key codes), window copy
 cudaError_t launch_seg_flush(const SegFlushParams& p, int dtype, int64_t max_tokens, cudaStream_t s);
 cudaError_t launch_seg_window(const SegFlushParams& p, int dtype, cudaStream_t s);

@@ -203,6 +203,7 @@ cudaError_t launch_prompt_simt(const PromptParams& p, int dtype, int64_t tiles, 
 cudaError_t launch_cross_simt(const CrossParams& p, int dtype, int64_t tiles, cudaStream_t s);
 // CTAs that share a tile of the CUDA-core attention
 int prompt_simt_split(int64_t tiles, int32_t max_len, int n_sm);
+int cross_simt_split(int64_t tiles, int32_t max_kv, int n_sm);
 cudaError_t launch_weights_simt(const PromptParams& p, int dtype, int64_t tiles, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, int32_t max_len, int32_t max_keep, cudaStream_t s);
 
