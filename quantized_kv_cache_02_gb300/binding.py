@@ -520,14 +520,13 @@ def _call_on(torch, device, fn, *args):
         _check(status)
 
 
-def _rows_like(torch, name, t, like, heads, tokens, dim):
-    """Strides of a [tokens, heads, dim] tensor with like's dtype and device (heads None: any)."""
-    shape, stride = t.shape, t.stride()
-    assert len(shape) == 3 and shape[0] == tokens and shape[2] == dim and heads in (None, shape[1]), \
-        f"expected {name} of shape {(tokens, heads or 'heads', dim)}, got {tuple(shape)}"
-    assert t.dtype == like.dtype and t.get_device() == like.get_device(), f"{name} must match the dtype and device of q"
-    assert stride[2] == 1, f"{name}'s last dimension must be contiguous"
-    return stride[0], stride[1]
+def _rows_like(name, t, like, device, heads, tokens, dim):
+    """Strides of a [tokens, heads, dim] tensor with like's dtype, on its device."""
+    assert t.shape == (tokens, heads, dim), f"expected {name} of shape {(tokens, heads, dim)}, got {tuple(t.shape)}"
+    assert t.dtype == like.dtype and t.get_device() == device, f"{name} must match the dtype and device of q"
+    token, head, channel = t.stride()
+    assert channel == 1, f"{name}'s last dimension must be contiguous"
+    return token, head
 
 
 def _dtype_of(torch, q):
@@ -547,6 +546,7 @@ def cross_attention(q, k, v, q_lens, kv_lens, kv_starts=None, out=None, lse=None
     import torch
     dtype = _dtype_of(torch, q)
     device, (tokens, heads, dim) = q.get_device(), q.shape
+    assert k.dim() == 3, "k must be a tensor [rows, heads, head_dim]"
     rows, kv_heads = k.shape[0], k.shape[1]
     lens, states = _counts(q_lens), _counts(kv_lens)
     assert len(states) == len(lens), f"expected {len(lens)} lengths in kv_lens, got {len(states)}"
@@ -555,12 +555,12 @@ def cross_attention(q, k, v, q_lens, kv_lens, kv_starts=None, out=None, lse=None
         c.kv_starts = starts = _counts(kv_starts)
         assert len(starts) == len(lens), f"expected {len(lens)} starts in kv_starts, got {len(starts)}"
     c.n_q_tokens, c.n_kv_tokens = tokens, rows
-    c.q_token_stride, c.q_head_stride = _rows_like(torch, "q", q, q, heads, tokens, dim)
-    c.k_token_stride, c.k_head_stride = _rows_like(torch, "k", k, q, kv_heads, rows, dim)
-    c.v_token_stride, c.v_head_stride = _rows_like(torch, "v", v, q, kv_heads, rows, dim)
+    c.q_token_stride, c.q_head_stride = _rows_like("q", q, q, device, heads, tokens, dim)
+    c.k_token_stride, c.k_head_stride = _rows_like("k", k, q, device, kv_heads, rows, dim)
+    c.v_token_stride, c.v_head_stride = _rows_like("v", v, q, device, kv_heads, rows, dim)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    c.out_token_stride, c.out_head_stride = _rows_like(torch, "out", out, q, heads, tokens, dim)
+        out = torch.empty_like(q)
+    c.out_token_stride, c.out_head_stride = _rows_like("out", out, q, device, heads, tokens, dim)
     if lse is None:
         lse = torch.empty((heads, tokens), dtype=torch.float32, device=q.device)
     else:
@@ -618,23 +618,29 @@ def rotary(q, k, positions, plan, q_out=None, k_out=None, inverse=False):
     assert positions.dtype == torch.int64 or positions.dtype == torch.int32, \
         f"positions must be int32 or int64, got {positions.dtype}"
     assert positions.get_device() == device, "positions must be on q's device"
-    shape, stride = tuple(positions.shape), positions.stride()
+    shape, stride = positions.shape, positions.stride()
     assert shape == (tokens, plan.n_axes) or (shape == (tokens,) and plan.n_axes == 1), \
-        f"expected positions of shape {(tokens, plan.n_axes)}, got {shape}"
-    pairs = [(q, "q", q_out)] if k is None else [(q, "q", q_out), (k, "k", k_out)]
+        f"expected positions of shape {(tokens, plan.n_axes)}, got {tuple(shape)}"
     assert k is not None or k_out is None, "k_out without k"
-    tensors, results = (kvq_rotary_tensor * 2)(), []
-    for t, (x, name, y) in zip(tensors, pairs):
-        t.in_token_stride, t.in_head_stride = _rows_like(torch, name, x, q, None, tokens, dim)
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        t.out_token_stride, t.out_head_stride = _rows_like(torch, name + "_out", y, q, x.shape[1], tokens, dim)
-        t.input, t.out, t.n_heads = x.data_ptr(), y.data_ptr(), x.shape[1]
-        results.append(y)
+    tensors = (kvq_rotary_tensor * 2)()
+    t = tensors[0]
+    t.in_token_stride, t.in_head_stride = _rows_like("q", q, q, device, heads, tokens, dim)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    t.out_token_stride, t.out_head_stride = _rows_like("q_out", q_out, q, device, heads, tokens, dim)
+    t.input, t.out, t.n_heads = q.data_ptr(), q_out.data_ptr(), heads
+    if k is not None:
+        assert k.dim() == 3, "k must be a tensor [tokens, heads, head_dim]"
+        t, heads = tensors[1], k.shape[1]
+        t.in_token_stride, t.in_head_stride = _rows_like("k", k, q, device, heads, tokens, dim)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        t.out_token_stride, t.out_head_stride = _rows_like("k_out", k_out, q, device, heads, tokens, dim)
+        t.input, t.out, t.n_heads = k.data_ptr(), k_out.data_ptr(), heads
     _call_on(torch, device, load_library().kvq_rotary, ctypes.byref(plan.c), positions.data_ptr(),
              8 if positions.dtype == torch.int64 else 4, stride[0], stride[1] if len(stride) > 1 else 0, tokens, dtype,
-             tensors, len(pairs), bool(inverse))
-    return (results[0], results[1]) if k is not None else (results[0], None)
+             tensors, 1 if k is None else 2, bool(inverse))
+    return q_out, k_out
 
 
 def kvq_kernel_launches() -> int:
@@ -662,6 +668,7 @@ class KVQCache:
         import torch
         self.torch = torch
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self._index = torch.cuda.current_device() if self.device.index is None else self.device.index
         self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self.cfg = make_config(batch, n_kv_heads, n_q_heads, head_dim, residual_len, group, qmax,
                                KVQ_BF16 if dtype == "bf16" else KVQ_FP32, eps)
@@ -688,7 +695,7 @@ class KVQCache:
                 self.handle = kvq_create(self.cfg, self.capacity, self._base, self.nbytes)
 
     def _stream(self):
-        return self.torch.cuda.current_stream(self.device).cuda_stream
+        return self.torch._C._cuda_getCurrentRawStream(self._index)
 
     def _check_input(self, t, shape):
         assert t.is_cuda and t.device == self.device, "input must live on the cache's device"

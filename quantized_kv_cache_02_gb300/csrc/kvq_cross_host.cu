@@ -110,7 +110,6 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
   int n_sm = 0;
   KVQ_TRY(kvq::sm_count(&n_sm));
   kvq::CrossParams p;
-  memset(&p, 0, sizeof p);
   p.D = d;
   p.Hq = c->n_q_heads;
   p.Hkv = c->n_kv_heads;
@@ -146,33 +145,38 @@ kvq_status cross_attention(const kvq_cross* c, const void* q, const void* k, con
     int step;
   } parts[2] = {{{seqs.begin(), many}, tc ? kvq::cross_rows_tokens(p.g) : kvq::cross_few_simt_step(p.g)},
                 {{many, seqs.end()}, tc ? kvq::prompt_tc_tokens(p.g) : kvq::kPromptRows / p.g}};
-  for (bool launch : {false, true}) {  // every refusal before the first launch
-    for (Part& part : parts) {
-      for (size_t at = 0; at < part.seqs.size(); at += kvq::kMaxSeqsPerLaunch) {
-        const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, part.seqs.size() - at);
-        const int64_t tiles = fill_tiles(part.seqs, at, n, p.Hkv, part.step, &p.tiles);
-        if (tiles > kMaxTiles / 16) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
-        if (!launch) continue;
-        const int32_t most = p.tiles.seq[0].kv_len;
-        cudaError_t e;
-        if (&part == parts && tc) {
-          p.split = kvq::cross_rows_split(tiles, most, n_sm);
-          e = kvq::launch_cross_rows(p, tiles, s);
-        } else if (&part == parts) {
-          int32_t tokens = 0;
-          for (int k = 0; k < n; ++k) tokens = std::max(tokens, p.tiles.seq[k].q_len);
-          p.split = kvq::cross_few_simt_split(tiles, most, n_sm);
-          e = kvq::launch_cross_few_simt(p, dtype, std::min(tokens, part.step) * p.g, tiles, s);
-        } else if (tc) {
-          p.split = kvq::cross_tc_split(d, tiles, most, n_sm);
-          e = kvq::launch_cross_tc(p, tiles, n_sm, s);
-        } else {
-          p.split = kvq::cross_simt_split(tiles, most, n_sm);
-          e = kvq::launch_cross_simt(p, dtype, tiles, s);
-        }
-        if (e != cudaSuccess) return cuda_fail(e, "cross attention launch");
-        kvq::count_launches(1);
+  // every refusal before the first launch
+  for (const Part& part : parts) {
+    int64_t tiles = 0;
+    for (size_t at = 0; at < part.seqs.size(); ++at) {
+      if (at % kvq::kMaxSeqsPerLaunch == 0) tiles = 0;
+      tiles += (int64_t)kvq::prompt_blocks(part.seqs[at].q_len, part.step) * p.Hkv;
+      if (tiles > kMaxTiles / 16) return fail(KVQ_EUNSUPPORTED, "too many tiles for one launch");
+    }
+  }
+  for (Part& part : parts) {
+    for (size_t at = 0; at < part.seqs.size(); at += kvq::kMaxSeqsPerLaunch) {
+      const int n = (int)std::min<size_t>(kvq::kMaxSeqsPerLaunch, part.seqs.size() - at);
+      const int64_t tiles = fill_tiles(part.seqs, at, n, p.Hkv, part.step, &p.tiles);
+      const int32_t most = p.tiles.seq[0].kv_len;
+      cudaError_t e;
+      if (&part == parts && tc) {
+        p.split = kvq::cross_rows_split(tiles, most, n_sm);
+        e = kvq::launch_cross_rows(p, tiles, s);
+      } else if (&part == parts) {
+        int32_t tokens = 0;
+        for (int k = 0; k < n; ++k) tokens = std::max(tokens, p.tiles.seq[k].q_len);
+        p.split = kvq::cross_few_simt_split(tiles, most, n_sm);
+        e = kvq::launch_cross_few_simt(p, dtype, std::min(tokens, part.step) * p.g, tiles, s);
+      } else if (tc) {
+        p.split = kvq::cross_tc_split(d, tiles, most, n_sm);
+        e = kvq::launch_cross_tc(p, tiles, n_sm, s);
+      } else {
+        p.split = kvq::cross_simt_split(tiles, most, n_sm);
+        e = kvq::launch_cross_simt(p, dtype, tiles, s);
       }
+      if (e != cudaSuccess) return cuda_fail(e, "cross attention launch");
+      kvq::count_launches(1);
     }
   }
   return KVQ_OK;

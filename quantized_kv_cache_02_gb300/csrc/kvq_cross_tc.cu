@@ -11,11 +11,11 @@
 //
 // Warps 0-3 and 4-7 run the softmax of tile 0 and 1, one row a thread; warp 8
 // issues the MMAs, warp 9 the TMA copies (two more fill the warpgroup, whose registers
-// go to the softmax).  Encoders' states are few (a text's 512 are four blocks), so what
+// go to the softmax); warps 12-15 write the outputs.  Encoders' states are few (a text's 512 are four blocks), so what
 // surrounds the blocks counts: the CTAs stay and take item after item, and the ends
 // overlap.  The next item's queries and first states are copied while the last
-// blocks run, its first Q K^T follows a tile's last P V at once, and a tile's
-// output leaves (through shared memory of its own) under the other tile's MMAs.
+// blocks run, its first Q K^T follows a tile's last P V at once, and an output leaves
+// (through warps and shared memory of its own) under the next item's blocks.
 // Few items of many states are split over a cluster (p.split CTAs, an equal run of
 // blocks each), whose outputs, maxima and sums meet through distributed shared
 // memory, in rank order.
@@ -33,11 +33,36 @@ namespace kvq {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kTcThreads = 384;
-// Registers a thread after the split of the launch's 3 x 168: a softmax thread
-// holds a whole row of scores.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kOutWarp = 12;
+// Registers a thread after the split of the launch's 4 x 128 (3 x 168 without output
+// warps): a softmax thread holds a whole row of scores.
+template <bool SPLIT>
+constexpr int kTcThreads = SPLIT ? 384 : 512;
+template <bool SPLIT>
+constexpr int kSoftmaxRegs = SPLIT ? 216 : 176;
+template <bool SPLIT>
+constexpr int kOtherRegs = SPLIT ? 72 : 88;
+constexpr int kOutRegs = 72;
 constexpr float kSlack = 8.f;
+
+// 16 consecutive 32-bit columns of this thread's lane, times a.
+__device__ __forceinline__ void tm_scale16(uint32_t at, float a) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+  tm_wait_ld();
+#pragma unroll
+  for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * a);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 
 template <int D>
 struct TcLayout {
@@ -46,8 +71,10 @@ struct TcLayout {
   static constexpr uint32_t kTile = kChunk * (D / 64);    // a Q, K or V tile
   static constexpr uint32_t kStageWarp = 32 * 128;        // 32 rows of 64 output channels
   static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kStage = kRing + kSlots * kTile, kBars = kStage + 8 * kStageWarp;
-  // barriers: full and empty per slot, the end, then per tile: Q full, Q empty, S, P (two halves), O, S read
-  static constexpr int kNBars = 2 * kSlots + 1 + 14;
+  static constexpr uint32_t kMl = kStage + 4 * kStageWarp;  // [tile][row] (m, l), behind the output warps' stages
+  // barriers: full and empty per slot, the end, then per tile: Q full, Q empty, S, P (two halves), O after a block, S
+  // read, O after an item, (m, l) written, O read
+  static constexpr int kNBars = 2 * kSlots + 1 + 20;
   static constexpr bool kApart = D == 64;                 // P beside S, not over it
   static constexpr uint32_t kBriefs = kBars + kNBars * 8 + 8;     // behind the tensor memory's address and the abort word
   static constexpr size_t kSmem = kBriefs + 16 + 1024;    // + alignment
@@ -93,7 +120,7 @@ struct Brief {
 
 // SPLIT: a cluster of p.split CTAs an item, one item a cluster; else items in turn.
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
     cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ TcMaps maps, int n_items) {
   using L = TcLayout<D>;
   extern __shared__ uint8_t tc_raw[];
@@ -102,7 +129,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kSlots;
   const uint32_t bar_end = bar_empty + 8 * L::kSlots, bar_q = bar_end + 8, bar_qfree = bar_q + 16,
-                 bar_s = bar_qfree + 16, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16;
+                 bar_s = bar_qfree + 16, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16, bar_e = bar_r + 16, bar_l = bar_e + 16, bar_free = bar_l + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   Brief* briefs = reinterpret_cast<Brief*>(smem + L::kBriefs);
@@ -125,6 +152,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bar_init(bar_p + 16 * i + 8, 4);
       bar_init(bar_o + 8 * i, 1);
       bar_init(bar_r + 8 * i, 4);
+      bar_init(bar_e + 8 * i, 1);
+      bar_init(bar_l + 8 * i, 4);
+      bar_init(bar_free + 8 * i, 4);
     }
     bar_init_fence();
   }
@@ -135,8 +165,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   pdl_release();
 
-  if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp >= kMmaWarp && warp < kOutWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<SPLIT>));
     if (warp == kCopyWarp) {
       // ============ copies (lane 0): per item Q_0, Q_1, then K_0, V_0, K_1, V_1 ... ====
       if (lane == 0) {
@@ -199,7 +229,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool one = elect_one();
       auto meet = [](bool ok) -> bool { return __all_sync(0xffffffffu, ok); };
       uint32_t ring = 0;                                  // of the current item's K_0
-      uint32_t ph_q = 0, ph_p = 0, ph_r = 0;              // the phase to wait for, bit i for tile i
+      uint32_t ph_q = 0, ph_p = 0, ph_r = 0, ph_f = 0;    // the phase to wait for, bit i for tile i
+      uint32_t used = 0;                                  // bit i: O_i holds an item's output
       bool ok = true;
       // Block -1 stands for the end of an item before the first (items come by falling
       // number of states).
@@ -271,6 +302,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          j > 0 || ks > 0);
               };
               ok = ok && bar_wait(bar_p + 16 * i, ph_p >> i & 1u, abort);
+              if (!SPLIT && j == 0) {  // O_i has been read
+                if (used >> i & 1u) {
+                  ok = ok && bar_wait(bar_free + 8 * i, ph_f >> i & 1u, abort);
+                  ph_f ^= 1u << i;
+                }
+                used |= 1u << i;
+              }
               tm_fence_after();
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
@@ -282,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int ks = 4; ks < 8; ++ks)
                 if (ks < steps) values(ks);
-              if (one && (L::kApart || end)) mma_commit(bar_o + 8 * i);
+              if (one && (L::kApart || end)) mma_commit((end ? bar_e : bar_o) + 8 * i);
             }
             if (!L::kApart) {
               tm_fence_before();
@@ -312,18 +350,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       cluster_sync();
       cluster_sync();
     }
-  } else {
+  } else if (warp < kMmaWarp) {
     // ============ softmax: tile i, one row a thread ===================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<SPLIT>));
     const int i = warp >> 2, r = t & 127;
-    const int tt = r / p.g, member = r - tt * p.g;
+    const int tt = r / p.g;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm + L::kColS + 128 * i + lanes, to = tm + L::kColO + D * i + lanes,
                    tp = tm + L::kColP + L::kStepP * i + lanes;
     const float2 sc = make_float2(p.scale2, p.scale2);
-    uint8_t* stage = smem + L::kStage + warp * L::kStageWarp;
-    float2* ml = reinterpret_cast<float2*>(smem + L::kStage);  // (split: of every row, in place of the stage)
-    uint32_t n_s = 0, n_o = 0;
+    float2* ml = reinterpret_cast<float2*>(smem + (SPLIT ? L::kStage : L::kMl));
+    uint32_t n_s = 0, n_o = 0, n_e = 0;
     bool ok = true;
     for (int x = x0; x < n_items && ok; x += dx) {
       int n, kv_len;
@@ -335,7 +372,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         kv_len = it.seq.kv_len;
         warp_live = __any_sync(0xffffffffu, tt < tile_tok && it.tok0 + i * tile_tok + tt < it.seq.q_len);
       }
+      if (n == 0 && !SPLIT) continue;
       float m = -FLT_MAX, l = 0.f;  // (not -INFINITY: scores of minus infinity may come first)
+      auto before_weights = [&](int j) {  // the last block's P V, or the last item's, is done with P (and with O)
+        bool done = true;
+        if (j > 0) done = warp_wait(bar_o + 8 * i, n_o++ & 1u, abort);
+        else if (n_e > 0) done = warp_wait(bar_e + 8 * i, (n_e - 1) & 1u, abort);
+        tm_fence_after();
+        return done;
+      };
       for (int j = 0; j < n; ++j, ++n_s) {
         if (!(ok = warp_wait(bar_s + 8 * i, n_s & 1u, abort))) break;
         if (warp_live) {
@@ -363,24 +408,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
           const bool up = top > m + kSlack;
-          if (L::kApart && j > 0) {  // the last block's P V is done with P and with O
-            if (!(ok = warp_wait(bar_o + 8 * i, n_o++ & 1u, abort))) break;
-            tm_fence_after();
-          }
+          if (L::kApart && !(ok = before_weights(j))) break;
           if (__any_sync(0xffffffffu, up)) {
             const float a = up ? ex2(m - top) : 1.f;
             if (up) m = top;
             l *= a;
             if (j > 0) {
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tm_ld32(to + 32 * c, o);
-                tm_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= a;
-                tm_st32(to + 32 * c, o);
-              }
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) tm_scale16(to + c, a);
             }
           }
           const float2 nm = make_float2(-m, -m);
@@ -407,58 +442,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (L::kApart) {
             // like the others, so that no arrival counts for the block before
             warp_arrive(bar_r + 8 * i);
-            if (j > 0 && !(ok = warp_wait(bar_o + 8 * i, n_o++ & 1u, abort))) break;
+            if (!(ok = before_weights(j))) break;
           }
           warp_arrive(bar_p + 16 * i);
         }
         warp_arrive(bar_p + 16 * i + 8);
       }
-      if (ok && n > 0) ok = warp_wait(bar_o + 8 * i, n_o++ & 1u, abort);
       if (!ok) break;
-      if (!warp_live) continue;
-      tm_fence_after();
       if constexpr (SPLIT) {
+        if (n > 0 && !(ok = warp_wait(bar_e + 8 * i, 0, abort))) break;
+        tm_fence_after();
         ml[t] = make_float2(m, l);
-        continue;
+      } else {
+        // the last item's have been read (else its phase of bar_l could pass unseen, too)
+        if (n_e > 0 && !(ok = warp_wait(bar_free + 8 * i, (n_e - 1) & 1u, abort))) break;
+        ml[t] = make_float2(m, l);
+        warp_arrive(bar_l + 8 * i);
       }
-      const Item it = item_at<SPLIT>(p, x);  // (again: kept over the blocks it would cost them registers)
-      const int pos = it.tok0 + i * tile_tok + tt, head = it.head * p.g + member;
-      const bool live = tt < tile_tok && pos < it.seq.q_len;
-      const float inv = 1.f / l;
-      __nv_bfloat16* dst =
-          static_cast<__nv_bfloat16*>(p.out) + (int64_t)(it.seq.q_start + pos) * p.o_ts + (int64_t)head * p.o_hs;
-      // 64 channels at a time through shared memory, 16-byte pieces swizzled by row,
-      // so that the warp stores whole rows
-      const uint32_t rows_live = __ballot_sync(0xffffffffu, live);
-#pragma unroll 1
-      for (int half = 0; half < D / 64; ++half) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float o[32];
-          tm_ld32(to + 64 * half + 32 * c, o);  // (without states anything, and not used)
-          tm_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = it.n > 0 ? o[e] * inv : 0.f;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((4 * c + e / 8) ^ (lane & 7)) * 16) =
-                make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
-                           pack_bf16(o[e + 6], o[e + 7]));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int y = lane; y < 32 * 8; y += 32) {
-          const int row = y / 8, c = y % 8;
-          const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (c ^ (row & 7)) * 16);
-          if (rows_live >> row & 1u) *reinterpret_cast<uint4*>(at + 128 * half + 16 * c) = v;
-        }
-        __syncwarp();
-      }
-      tm_fence_before();
-      if (live && p.lse)
-        p.lse[(int64_t)head * p.n_tokens + it.seq.q_start + pos] =
-            it.n > 0 ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+      ++n_e;
     }
     if (!ok) {
       *abort = 1;
@@ -518,6 +519,76 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       cluster_sync();  // no CTA ends while another reads its outputs
     }
+  } else {
+    // ============ outputs: an item's O_0, then its O_1, one row a thread =================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+    const int r = t & 127, tt = r / p.g, member = r - tt * p.g;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    uint8_t* stage = smem + L::kStage + (warp & 3) * L::kStageWarp;
+    const float2* ml = reinterpret_cast<const float2*>(smem + L::kMl);
+    uint32_t done = 0;  // bit i: the phase to wait for of tile i
+    bool ok = true;
+    for (int x = x0; x < n_items && ok; x += dx) {
+      const Item it = item_at<SPLIT>(p, x);
+#pragma unroll 1
+      for (int i = 0; i < (it.two ? 2 : 1); ++i) {
+        const int pos = it.tok0 + i * tile_tok + tt, head = it.head * p.g + member;
+        const bool live = tt < tile_tok && pos < it.seq.q_len;
+        const uint32_t rows_live = __ballot_sync(0xffffffffu, live), phase = done >> i & 1u;
+        float inv = 0.f, lse = -INFINITY;  // without states
+        if (it.n > 0) {
+          if (!(ok = warp_wait(bar_l + 8 * i, phase, abort) && warp_wait(bar_e + 8 * i, phase, abort))) break;
+          done ^= 1u << i;
+          tm_fence_after();
+          const float2 row = ml[128 * i + r];
+          inv = 1.f / row.y;
+          lse = (row.x + log2f(row.y)) * 0.69314718055994530942f;
+        }
+        if (rows_live) {
+          __nv_bfloat16* dst =
+              static_cast<__nv_bfloat16*>(p.out) + (int64_t)(it.seq.q_start + pos) * p.o_ts + (int64_t)head * p.o_hs;
+          const uint32_t to = tm + L::kColO + D * i + lanes;
+          // 64 channels at a time through shared memory, 16-byte pieces swizzled by row,
+          // so that the warp stores whole rows
+#pragma unroll 1
+          for (int half = 0; half < D / 64; ++half) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              float o[32];
+              tm_ld32(to + 64 * half + 32 * c, o);  // (without states anything, and not used)
+              tm_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = it.n > 0 ? o[e] * inv : 0.f;
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((4 * c + e / 8) ^ (lane & 7)) * 16) =
+                    make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
+                               pack_bf16(o[e + 6], o[e + 7]));
+            }
+            if (half == D / 64 - 1 && it.n > 0) {
+              tm_fence_before();
+              warp_arrive(bar_free + 8 * i);  // O_i has been read
+            }
+            __syncwarp();
+#pragma unroll
+            for (int y = lane; y < 32 * 8; y += 32) {
+              const int row = y / 8, c = y % 8;
+              const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (c ^ (row & 7)) * 16);
+              if (rows_live >> row & 1u) *reinterpret_cast<uint4*>(at + 128 * half + 16 * c) = v;
+            }
+            __syncwarp();
+          }
+          if (live && p.lse) p.lse[(int64_t)head * p.n_tokens + it.seq.q_start + pos] = lse;
+        } else if (it.n > 0) {
+          warp_arrive(bar_free + 8 * i);
+        }
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      if (p.status && lane == 0) atomicOr(p.status, kStatusPromptTimeout);
+    }
   }
   tm_fence_before();
   __syncthreads();
@@ -533,7 +604,7 @@ cudaError_t launch_tc(const CrossParams& p, const TcMaps& maps, int64_t tiles, i
   const cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)TcLayout<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_cluster(cross_tc_kernel<D, SPLIT>, SPLIT || tiles < n_sm ? tiles : n_sm, p.split, kTcThreads,
+  return launch_cluster(cross_tc_kernel<D, SPLIT>, SPLIT || tiles < n_sm ? tiles : n_sm, p.split, kTcThreads<SPLIT>,
                         TcLayout<D>::kSmem, s, p, maps, (int)tiles);
 }
 
@@ -545,7 +616,7 @@ int split_of(int64_t tiles, int32_t max_kv, int n_sm) {
   const int64_t blocks = (max_kv + kKeys - 1) / kKeys;
   for (int split = 8; split > 1; --split)
     if (tiles * split <= n_sm && blocks >= 2 * split &&
-        tiles <= active_clusters<cross_tc_kernel<D, true>>(split, kTcThreads, TcLayout<D>::kSmem))
+        tiles <= active_clusters<cross_tc_kernel<D, true>>(split, kTcThreads<true>, TcLayout<D>::kSmem))
       return split;
   return 1;
 }

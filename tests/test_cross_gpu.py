@@ -233,3 +233,15 @@ def test_split_states_minus_infinity(torch, kvq):
         check(torch, out, lse, q, k[2900:], v[2900:], [n], [100])
         out, lse = kvq.cross_attention(q, k, v, [n], [2900])
         assert out.isnan().all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (16, 4, 128), (7, 1, 128), (6, 6, 128)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([9000], [100]), ([20000], [128]), ([5000, 3000, 1, 6000], [300, 0, 40, 129]),
+                                            ([2500] * 8, [64, 700, 128, 1, 256, 513, 16, 1000])])
+def test_more_tiles_than_ctas(torch, kvq, hq, hkv, d, q_lens, kv_lens):
+    """CTAs that take tile after tile, of one block of states and of several."""
+    q, k, v = inputs(torch, sum(q_lens), sum(kv_lens), hq, hkv, d, "bfloat16", 5)
+    for _ in range(3):
+        out, lse = kvq.cross_attention(q, k, v, q_lens, kv_lens)
+    check(torch, out, lse, q, k, v, q_lens, kv_lens)
+    assert kvq.prompt_status() == 0
