@@ -16,6 +16,11 @@
 // warps, so no workspace, no atomics and the same bits each time
 // ("KV Cache 与自回归视频生成" section 05, FlashDecoding).
 //
+// An MMA takes operands of one type, so weights meet bf16 Values as bf16: off by at most
+// 2^-8 of each, the output by 2.3e-3 (relative norm) where fp32 weights leave its own rounding's 1.7e-3.
+// (A second product on what the rounding leaves would hide under the copies, but
+// turn an infinite Value into NaN.)
+//
 // Bound: HBM, the states read once.  mma.sync and not tcgen05: 16 rows would leave
 // seven eighths of a 128-row accumulator empty, and the copies take longer than these.
 
