@@ -27,6 +27,9 @@
  *    quantized prefix is dequantized in registers; the split over the sequence
  *    and the merge of partial softmax states follow section 05 (FlashDecoding).
  *  - Byte ledger: "KV Cache 量化与压缩" (xuujii M005) sections 01 and 05.
+ *  - In front of the cache and beside it: causal prompt attention, gathered
+ *    weights and eviction; rotary positions, attention over an encoder's states,
+ *    and forks of cached sequences (their formulas at their functions).
  *
  * Conventions for every entry point:
  *  - Status codes: KVQ_OK on success; any other value leaves the cache state

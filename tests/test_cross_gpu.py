@@ -245,3 +245,19 @@ def test_more_tiles_than_ctas(torch, kvq, hq, hkv, d, q_lens, kv_lens):
         out, lse = kvq.cross_attention(q, k, v, q_lens, kv_lens)
     check(torch, out, lse, q, k, v, q_lens, kv_lens)
     assert kvq.prompt_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 200])
+@pytest.mark.parametrize("dtype,d", [("bfloat16", 64), ("float32", 64)])
+def test_offsets_past_32_bits(torch, kvq, dtype, d, n):
+    """States whose rows lie a megabyte apart: the last ones past 2^32 elements."""
+    m, step = 4200, 1 << 20
+    dt = getattr(torch, dtype)
+    buffer = torch.empty(m * step, dtype=dt, device="cuda")
+    k, v = (buffer.as_strided((m, 2, d), (step, d, 1), at) for at in (0, step // 2))
+    q, kk, vv = inputs(torch, n, m, 4, 2, d, dtype)
+    k.copy_(kk), v.copy_(vv)
+    out, lse = kvq.cross_attention(q, k, v, [n], [m])
+    want, want_lse = kvq.cross_attention(q, kk, vv, [n], [m])
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    check(torch, out, lse, q, kk, vv, [n], [m])

@@ -190,3 +190,18 @@ def test_on_a_side_stream(torch, kvq):
         ks, vs = cache.restore()
     side.synchronize()
     assert torch.equal(ks[1], ks[0]) and torch.equal(vs[2], vs[0]) and cache.device_status() == 0
+
+
+def test_offsets_past_32_bits(torch, kvq):
+    """Sequences whose pages lie past 2^32 bytes of the arena."""
+    c = dict(d=128, R=128, G=64, qmax=127, dtype="bf16", hkv=8, hq=8)
+    n = 1000
+    cache = make(kvq, "contiguous", c, [1200000, 1200, 1200, 1200000, 1200])
+    k, v = rows(torch, c, n, 3)
+    cache.append(k, v, 1)
+    cache.fork([1, 1], [3, 4])
+    ks, vs = cache.restore()
+    for b in (3, 4):
+        assert torch.equal(ks[b, :, :n], ks[1, :, :n]) and torch.equal(vs[b, :, :n], vs[1, :, :n])
+    cache.fork([4, 3], [0, 4])
+    assert everything(cache, c, 1)[0][1] == everything(cache, c, 2)[1][1]

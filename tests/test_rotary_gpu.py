@@ -203,3 +203,18 @@ def test_refusals(torch, kvq):
         kvq.rotary(wide[:4, :, :64], None, at[:4], plan, q_out=wide.view(16, 2, 128)[:4].view(4, 4, 64))
     with pytest.raises(kvq.KVQError):  # rows one over the other
         kvq.rotary(q, None, at, plan, q_out=wide.view(-1)[:64].expand(8, 4, 64))
+
+
+@pytest.mark.parametrize("interleaved,pairs", [(False, 16), (True, 13), (False, 13)])
+def test_offsets_past_32_bits(torch, kvq, interleaved, pairs):
+    """Rows that lie a megabyte apart: the last ones past 2^32 elements."""
+    tokens, step = 4200, 1 << 20
+    buffer = torch.empty(tokens * step, dtype=torch.bfloat16, device="cuda")
+    q, out = (buffer.as_strided((tokens, 2, 64), (step, 64, 1), at) for at in (0, step // 2))
+    x = normal(torch, (tokens, 2, 64), "bfloat16")
+    q.copy_(x)
+    plan = kvq.Rotary.sections(64, [pairs], interleaved=interleaved)
+    at = torch.arange(tokens, device="cuda")
+    kvq.rotary(q, None, at, plan, q_out=out)
+    assert torch.equal(out, kvq.rotary(x, None, at, plan)[0]) and torch.equal(q, x)
+    check(torch, out, x, at, plan)
