@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import numbers
 import os
+from array import array
 from operator import index
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,7 +75,7 @@ class kvq_prompt(ctypes.Structure):
 
 class kvq_cross(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_q_heads", "n_kv_heads", "head_dim", "dtype")] + [
-        (n, ctypes.POINTER(ctypes.c_int64)) for n in ("q_lens", "kv_lens", "kv_starts")] + [
+        (n, ctypes.c_void_p) for n in ("q_lens", "kv_lens", "kv_starts")] + [  # (addresses: quicker to fill in)
         (n, ctypes.c_int64) for n in ("n_q_tokens", "n_kv_tokens", "q_token_stride", "q_head_stride", "k_token_stride",
                                       "k_head_stride", "v_token_stride", "v_head_stride", "out_token_stride",
                                       "out_head_stride")] + [("status", ctypes.c_void_p)]
@@ -509,30 +510,41 @@ def evict(k, v, weights, seq_lens, keep, first=0, recent=0):
 
 
 # ---- beside the cache: cross attention, rotary positions --------------------------
+#
+# As the prompt operators, bound by the host when small.
 
-def _call_on(torch, device, fn, *args):
+_torch = None
+
+
+def _call_on(device, fn, *args):
     """fn(*args, torch's current stream on device), with that device current."""
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
-            return _call_on(torch, device, fn, *args)
-    status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if _torch._C._cuda_getDevice() != device:
+        with _torch.cuda.device(device):
+            return _call_on(device, fn, *args)
+    status = fn(*args, _torch._C._cuda_getCurrentRawStream(device))
     if status:
         _check(status)
 
 
-def _rows_like(name, t, like, device, heads, tokens, dim):
-    """Strides of a [tokens, heads, dim] tensor with like's dtype, on its device."""
-    assert t.shape == (tokens, heads, dim), f"expected {name} of shape {(tokens, heads, dim)}, got {tuple(t.shape)}"
-    assert t.dtype == like.dtype and t.get_device() == device, f"{name} must match the dtype and device of q"
+def _queries(q):
+    """(kvq dtype, torch dtype, device index, shape) of q, the tensor that the others go by."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    dtype, shape = q.dtype, q.shape
+    assert q.is_cuda and len(shape) == 3, "q must be a CUDA tensor [tokens, heads, head_dim]"
+    assert dtype == _torch.bfloat16 or dtype == _torch.float32, f"expected bfloat16 or float32, got {dtype}"
+    return KVQ_BF16 if dtype == _torch.bfloat16 else KVQ_FP32, dtype, q.get_device(), shape
+
+
+def _rows(name, t, shape, dtype, device):
+    """Token and head strides of a tensor of this shape [tokens, heads, dim], q's dtype and device."""
+    assert t.shape == shape, f"expected {name} of shape {tuple(shape)}, got {tuple(t.shape)}"
+    assert t.dtype == dtype and t.get_device() == device, f"{name} must match the dtype and device of q"
     token, head, channel = t.stride()
     assert channel == 1, f"{name}'s last dimension must be contiguous"
     return token, head
-
-
-def _dtype_of(torch, q):
-    assert q.is_cuda and q.dim() == 3, "q must be a CUDA tensor [tokens, heads, head_dim]"
-    assert q.dtype == torch.bfloat16 or q.dtype == torch.float32, f"expected bfloat16 or float32, got {q.dtype}"
-    return KVQ_BF16 if q.dtype == torch.bfloat16 else KVQ_FP32
 
 
 def cross_attention(q, k, v, q_lens, kv_lens, kv_starts=None, out=None, lse=None):
@@ -543,36 +555,37 @@ def cross_attention(q, k, v, q_lens, kv_lens, kv_starts=None, out=None, lse=None
     may repeat, so sequences can share states).  Returns (out, lse): out like q,
     lse float32 [n_q_heads, tokens]; over no states 0 and minus infinity.
     q_lens of 1 is the form for single tokens.  No gradient."""
-    import torch
-    dtype = _dtype_of(torch, q)
-    device, (tokens, heads, dim) = q.get_device(), q.shape
-    assert k.dim() == 3, "k must be a tensor [rows, heads, head_dim]"
-    rows, kv_heads = k.shape[0], k.shape[1]
-    lens, states = _counts(q_lens), _counts(kv_lens)
-    assert len(states) == len(lens), f"expected {len(lens)} lengths in kv_lens, got {len(states)}"
-    c = kvq_cross(len(lens), heads, kv_heads, dim, dtype, lens, states)
+    code, dtype, device, shape = _queries(q)
+    tokens, heads, dim = shape
+    kv_shape = k.shape
+    assert len(kv_shape) == 3 and kv_shape[2] == dim, f"k of shape {tuple(kv_shape)} does not go with q of {tuple(shape)}"
+    lens, states = array("q", q_lens), array("q", kv_lens)  # (a fraction is no count)
+    n = len(lens)
+    assert len(states) == n, f"expected {n} lengths in kv_lens, got {len(states)}"
+    c = kvq_cross(n, heads, kv_shape[1], dim, code, lens.buffer_info()[0], states.buffer_info()[0])
     if kv_starts is not None:
-        c.kv_starts = starts = _counts(kv_starts)
-        assert len(starts) == len(lens), f"expected {len(lens)} starts in kv_starts, got {len(starts)}"
-    c.n_q_tokens, c.n_kv_tokens = tokens, rows
-    c.q_token_stride, c.q_head_stride = _rows_like("q", q, q, device, heads, tokens, dim)
-    c.k_token_stride, c.k_head_stride = _rows_like("k", k, q, device, kv_heads, rows, dim)
-    c.v_token_stride, c.v_head_stride = _rows_like("v", v, q, device, kv_heads, rows, dim)
+        starts = array("q", kv_starts)
+        assert len(starts) == n, f"expected {n} starts in kv_starts, got {len(starts)}"
+        c.kv_starts = starts.buffer_info()[0]
+    c.n_q_tokens, c.n_kv_tokens = tokens, kv_shape[0]
+    c.q_token_stride, c.q_head_stride = _rows("q", q, shape, dtype, device)
+    c.k_token_stride, c.k_head_stride = _rows("k", k, kv_shape, dtype, device)
+    c.v_token_stride, c.v_head_stride = _rows("v", v, kv_shape, dtype, device)
     if out is None:
-        out = torch.empty_like(q)
-    c.out_token_stride, c.out_head_stride = _rows_like("out", out, q, device, heads, tokens, dim)
+        out = _torch.empty_like(q)
+    c.out_token_stride, c.out_head_stride = _rows("out", out, shape, dtype, device)
     if lse is None:
-        lse = torch.empty((heads, tokens), dtype=torch.float32, device=q.device)
+        lse = _torch.empty((heads, tokens), dtype=_torch.float32, device=q.device)
     else:
-        assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.get_device() == device and \
+        assert lse.dtype == _torch.float32 and lse.is_contiguous() and lse.get_device() == device and \
             lse.shape == (heads, tokens), f"lse must be a contiguous float32 tensor {(heads, tokens)} on q's device"
     word = _prompt_status.get(device)
     if word is None:
         word = _status_word(device)
     if word is not None:
         c.status = word.data_ptr()
-    _call_on(torch, device, load_library().kvq_cross_attention, ctypes.byref(c), q.data_ptr(), k.data_ptr(),
-             v.data_ptr(), out.data_ptr(), lse.data_ptr())
+    _call_on(device, load_library().kvq_cross_attention, ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             out.data_ptr(), lse.data_ptr())
     return out, lse
 
 
@@ -591,6 +604,7 @@ class Rotary:
         self.n_axes = max(axes) + 1
         self.c = kvq_rotary_plan(self.head_dim, self.n_axes, len(axes), self.interleaved,
                                  (ctypes.c_double * len(axes))(*frequencies), (ctypes.c_int32 * len(axes))(*axes))
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def sections(cls, head_dim, sections, theta=10000.0, restart=False, interleaved=False):
@@ -611,35 +625,37 @@ def rotary(q, k, positions, plan, q_out=None, k_out=None, inverse=False):
     n_axes], or [tokens] for one axis; any values) by a Rotary plan, in one launch.
     Returns (q_out, k_out), made where None; q_out=q and k_out=k turn in place.
     inverse turns back: it undoes the call, and takes gradients through it."""
-    import torch
-    dtype = _dtype_of(torch, q)
-    device, (tokens, heads, dim) = q.get_device(), q.shape
+    code, dtype, device, shape = _queries(q)
+    tokens, heads, dim = shape
     assert dim == plan.head_dim, f"q has heads of {dim} channels, the plan of {plan.head_dim}"
-    assert positions.dtype == torch.int64 or positions.dtype == torch.int32, \
-        f"positions must be int32 or int64, got {positions.dtype}"
+    wide = positions.dtype == _torch.int64
+    assert wide or positions.dtype == _torch.int32, f"positions must be int32 or int64, got {positions.dtype}"
     assert positions.get_device() == device, "positions must be on q's device"
-    shape, stride = positions.shape, positions.stride()
-    assert shape == (tokens, plan.n_axes) or (shape == (tokens,) and plan.n_axes == 1), \
-        f"expected positions of shape {(tokens, plan.n_axes)}, got {tuple(shape)}"
-    assert k is not None or k_out is None, "k_out without k"
+    at = positions.shape
+    assert at == (tokens, plan.n_axes) or (at == (tokens,) and plan.n_axes == 1), \
+        f"expected positions of shape {(tokens, plan.n_axes)}, got {tuple(at)}"
+    steps = positions.stride()
     tensors = (kvq_rotary_tensor * 2)()
     t = tensors[0]
-    t.in_token_stride, t.in_head_stride = _rows_like("q", q, q, device, heads, tokens, dim)
+    t.in_token_stride, t.in_head_stride = _rows("q", q, shape, dtype, device)
     if q_out is None:
-        q_out = torch.empty_like(q)
-    t.out_token_stride, t.out_head_stride = _rows_like("q_out", q_out, q, device, heads, tokens, dim)
+        q_out = _torch.empty_like(q)
+    t.out_token_stride, t.out_head_stride = _rows("q_out", q_out, shape, dtype, device)
     t.input, t.out, t.n_heads = q.data_ptr(), q_out.data_ptr(), heads
     if k is not None:
-        assert k.dim() == 3, "k must be a tensor [tokens, heads, head_dim]"
-        t, heads = tensors[1], k.shape[1]
-        t.in_token_stride, t.in_head_stride = _rows_like("k", k, q, device, heads, tokens, dim)
+        shape = k.shape
+        assert len(shape) == 3 and shape[0] == tokens and shape[2] == dim, \
+            f"k of shape {tuple(shape)} does not go with q of shape {tuple(q.shape)}"
+        t = tensors[1]
+        t.in_token_stride, t.in_head_stride = _rows("k", k, shape, dtype, device)
         if k_out is None:
-            k_out = torch.empty_like(k)
-        t.out_token_stride, t.out_head_stride = _rows_like("k_out", k_out, q, device, heads, tokens, dim)
-        t.input, t.out, t.n_heads = k.data_ptr(), k_out.data_ptr(), heads
-    _call_on(torch, device, load_library().kvq_rotary, ctypes.byref(plan.c), positions.data_ptr(),
-             8 if positions.dtype == torch.int64 else 4, stride[0], stride[1] if len(stride) > 1 else 0, tokens, dtype,
-             tensors, 1 if k is None else 2, bool(inverse))
+            k_out = _torch.empty_like(k)
+        t.out_token_stride, t.out_head_stride = _rows("k_out", k_out, shape, dtype, device)
+        t.input, t.out, t.n_heads = k.data_ptr(), k_out.data_ptr(), shape[1]
+    else:
+        assert k_out is None, "k_out without k"
+    _call_on(device, load_library().kvq_rotary, plan.ref, positions.data_ptr(), 8 if wide else 4, steps[0],
+             steps[1] if len(steps) > 1 else 0, tokens, code, tensors, 1 if k is None else 2, bool(inverse))
     return q_out, k_out
 
 

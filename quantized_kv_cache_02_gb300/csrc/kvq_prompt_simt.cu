@@ -32,7 +32,6 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSimtFill = 2;
 constexpr int kPStride = kPromptKeys + 4;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -401,7 +400,7 @@ int prompt_simt_split(int64_t tiles, int32_t max_len, int n_sm) {
 // over 777 states 66.7 us with two CTAs a tile, 55.6 with four).
 int cross_simt_split(int64_t tiles, int32_t max_kv, int n_sm) {
   int split = 1;
-  while (split < 8 && tiles * split < kSimtFill * (int64_t)n_sm && max_kv >= 2 * split * kPromptKeys) split *= 2;
+  while (split < 8 && tiles * split < 2 * (int64_t)n_sm && max_kv >= 2 * split * kPromptKeys) split *= 2;
   return split;
 }
 

@@ -26,10 +26,11 @@ def cross(q_lens=(5, 0, 3), kv_lens=(4, 2, 6), kv_starts=None, **kw):
     a = dict(n_q_heads=8, n_kv_heads=2, head_dim=64, dtype=B.KVQ_BF16, n_q_tokens=8, n_kv_tokens=12, n_seqs=len(q_lens))
     a.update(kw)
     keep = [i64(q_lens), i64(kv_lens)]
-    c = B.kvq_cross(a["n_seqs"], a["n_q_heads"], a["n_kv_heads"], a["head_dim"], a["dtype"], *keep)
+    c = B.kvq_cross(a["n_seqs"], a["n_q_heads"], a["n_kv_heads"], a["head_dim"], a["dtype"],
+                    *[ctypes.addressof(x) for x in keep])
     if kv_starts is not None:
         keep.append(i64(kv_starts))
-        c.kv_starts = keep[-1]
+        c.kv_starts = ctypes.addressof(keep[-1])
     c.n_q_tokens, c.n_kv_tokens = a["n_q_tokens"], a["n_kv_tokens"]
     for t, h in (("q", 8), ("k", 2), ("v", 2), ("out", 8)):
         setattr(c, f"{t}_token_stride", a.get(f"{t}_token_stride", h * 64))
