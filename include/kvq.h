@@ -583,7 +583,7 @@ kvq_status kvq_cross_attention(const kvq_cross* cross, const void* q, const void
  * positions: device integers of position_bytes (4 or 8) bytes, element (token, axis)
  * at token * position_token_stride + axis * position_axis_stride; any value, negative
  * ones too.  Angles come from integer arithmetic modulo whole turns: those of far
- * positions are as good as those of near ones (within 2^-32 of a turn for positions
+ * positions are as good as those of near ones (within 2^-31 of a turn for positions
  * up to 2^32, beside the frequency's own rounding to 2^-53 of itself).  Products
  * and sums are fp32, rounded once to dtype.  Channels past the pairs are copied.
  * Only enqueues work on ``stream``; no workspace.  An out that is not its own input

@@ -255,6 +255,11 @@ cudaError_t launch_r(const CrossParams& p, int64_t tiles, cudaStream_t s) {
   if (p.split > 8) {
     const cudaError_t wide = cudaFuncSetAttribute(cross_few_kernel<T, R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (wide != cudaSuccess) return wide;
+    if (active_clusters<cross_few_kernel<T, R>>(p.split, kThreads, few_smem<T>(p.D), p.D / 16) < tiles) {
+      CrossParams q = p;
+      q.split = 8;
+      return launch_r<T, R>(q, tiles, s);
+    }
   }
   return launch_cluster(cross_few_kernel<T, R>, tiles, p.split, kThreads, few_smem<T>(p.D), s, p);
 }

@@ -270,6 +270,11 @@ cudaError_t launch_rows(const CrossParams& p, const RowsMaps& maps, int64_t tile
   if (p.split > 8) {
     const cudaError_t wide = cudaFuncSetAttribute(cross_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (wide != cudaSuccess) return wide;
+    if (active_clusters<cross_rows_kernel<D>>(p.split, kRowsThreads, RowsLayout<D>::kSmem) < tiles) {
+      CrossParams q = p;
+      q.split = 8;
+      return launch_rows<D>(q, maps, tiles, s);
+    }
   }
   return launch_cluster(cross_rows_kernel<D>, tiles, p.split, kRowsThreads, RowsLayout<D>::kSmem, s, p, maps);
 }

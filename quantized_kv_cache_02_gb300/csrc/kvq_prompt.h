@@ -172,13 +172,14 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int64_t tiles, int split, 
 }
 
 // Clusters of ``size`` CTAs of a kernel that run at once on the current device, asked
-// for once a size; 0 if unknown.
+// for once a size and ``kind`` (0..16: calls of one kind have the same shared memory);
+// 0 if unknown.
 template <auto KERNEL>
-int active_clusters(int size, int threads, size_t smem) {
-  static std::atomic<int> known[64][17];
+int active_clusters(int size, int threads, size_t smem, int kind = 0) {
+  static std::atomic<int> known[64][17][17];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || size > 16) return 0;
-  int n = known[dev][size].load();
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || size > 16 || kind > 16) return 0;
+  int n = known[dev][size][kind].load();
   if (n) return n - 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)size);
@@ -194,7 +195,7 @@ int active_clusters(int size, int threads, size_t smem) {
     cudaGetLastError();
     return 0;
   }
-  known[dev][size].store(n + 1);
+  known[dev][size][kind].store(n + 1);
   return n;
 }
 
