@@ -261,3 +261,17 @@ def test_offsets_past_32_bits(torch, kvq, dtype, d, n):
     want, want_lse = kvq.cross_attention(q, kk, vv, [n], [m])
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     check(torch, out, lse, q, kk, vv, [n], [m])
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (8, 2, 128)])
+def test_mixed_sequences(torch, kvq, hq, hkv, d):
+    """One call of two launches: a token, few queries over many states, many queries over
+    fewer."""
+    q_lens, kv_lens = [1500, 40, 1, 60, 2, 700], [200, 4000, 1000, 6000, 0, 129]
+    q, k, v = inputs(torch, sum(q_lens), sum(kv_lens), hq, hkv, d, "bfloat16", 8)
+    before = kvq.kvq_kernel_launches()
+    out, lse = kvq.cross_attention(q, k, v, q_lens, kv_lens)
+    assert kvq.kvq_kernel_launches() == before + 2
+    check(torch, out, lse, q, k, v, q_lens, kv_lens)
+    again, _ = kvq.cross_attention(q, k, v, q_lens, kv_lens)
+    assert torch.equal(out, again) and kvq.prompt_status() == 0
