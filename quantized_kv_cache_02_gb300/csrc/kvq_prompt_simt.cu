@@ -32,6 +32,7 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kLoads = 4;  // 16-byte loads a thread has in flight
 constexpr int kPStride = kPromptKeys + 4;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -56,15 +57,26 @@ __device__ __forceinline__ bool load_keys(float* dst, int stride, int cols, cons
                                           int end, int D) {
   bool dirty = false;
   const int per = cols / 4;
-  for (int i = threadIdx.x; i < kPromptKeys * per; i += kThreads) {
-    const int r = i / per, c = (i - r * per) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (key0 + r < end && c < D) x = load4(base + (int64_t)(key0 + r) * ts + c);
-    if (CLEAN && !(finite(x.x) && finite(x.y) && finite(x.z) && finite(x.w))) {
-      dirty = true;
-      x = make_float4(finite(x.x) ? x.x : 0.f, finite(x.y) ? x.y : 0.f, finite(x.z) ? x.z : 0.f, finite(x.w) ? x.w : 0.f);
+  // several loads in flight (300 tokens of 64 channels 33.9 -> 29.6 us)
+  for (int i0 = threadIdx.x; i0 < kPromptKeys * per; i0 += kLoads * kThreads) {
+    float4 x[kLoads];
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int i = i0 + e * kThreads, r = i / per, c = (i - r * per) * 4;
+      x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < kPromptKeys && key0 + r < end && c < D) x[e] = load4(base + (int64_t)(key0 + r) * ts + c);
     }
-    *reinterpret_cast<float4*>(dst + r * stride + c) = x;
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int i = i0 + e * kThreads, r = i / per, c = (i - r * per) * 4;
+      if (r >= kPromptKeys) break;
+      float4& y = x[e];
+      if (CLEAN && !(finite(y.x) && finite(y.y) && finite(y.z) && finite(y.w))) {
+        dirty = true;
+        y = make_float4(finite(y.x) ? y.x : 0.f, finite(y.y) ? y.y : 0.f, finite(y.z) ? y.z : 0.f, finite(y.w) ? y.w : 0.f);
+      }
+      *reinterpret_cast<float4*>(dst + r * stride + c) = y;
+    }
   }
   return dirty;
 }
@@ -75,12 +87,20 @@ template <typename T>
 __device__ __forceinline__ void load_queries(float* dst, int stride, const AttentionParams& p, const T* q, int tok0,
                                              int tile_tok, int len, int h) {
   const int per = p.D / 4;
-  for (int i = threadIdx.x; i < kPromptRows * per; i += kThreads) {
-    const int r = i / per, c = (i - r * per) * 4, t = r / p.g;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t < tile_tok && tok0 + t < len)
-      x = load4(q + (int64_t)(tok0 + t) * p.q_ts + (int64_t)(h * p.g + r - t * p.g) * p.q_hs + c);
-    *reinterpret_cast<float4*>(dst + r * stride + c) = x;
+  for (int i0 = threadIdx.x; i0 < kPromptRows * per; i0 += kLoads * kThreads) {
+    float4 x[kLoads];
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int i = i0 + e * kThreads, r = i / per, c = (i - r * per) * 4, t = r / p.g;
+      x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < kPromptRows && t < tile_tok && tok0 + t < len)
+        x[e] = load4(q + (int64_t)(tok0 + t) * p.q_ts + (int64_t)(h * p.g + r - t * p.g) * p.q_hs + c);
+    }
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int i = i0 + e * kThreads, r = i / per, c = (i - r * per) * 4;
+      if (r < kPromptRows) *reinterpret_cast<float4*>(dst + r * stride + c) = x[e];
+    }
   }
 }
 
