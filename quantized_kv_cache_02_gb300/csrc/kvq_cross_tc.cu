@@ -11,11 +11,20 @@
 //
 // Warps 0-3 and 4-7 run the softmax of tile 0 and 1, one row a thread; warp 8
 // issues the MMAs, warp 9 the TMA copies (two more fill the warpgroup, whose registers
-// go to the softmax); warps 12-15 write the outputs.  Encoders' states are few (a text's 512 are four blocks), so what
+// go to the softmax).  Encoders' states are few (a text's 512 are four blocks), so what
 // surrounds the blocks counts: the CTAs stay and take item after item, and the ends
 // overlap.  The next item's queries and first states are copied while the last
-// blocks run, its first Q K^T follows a tile's last P V at once, and an output leaves
-// (through warps and shared memory of its own) under the next item's blocks.
+// blocks run, and its first Q K^T follows a tile's last P V at once.  At d = 128 warps
+// 12-15 write the outputs under the next item's blocks (14400 tokens over 512 states of
+// 32/8 heads 120 -> 111 us, 1.09 PFLOP/s); at d = 64, bound by the softmax, its warps do it
+// themselves (they are slower with the registers that four more warps leave them: 2048
+// states 171 us, 160 without).
+//
+// Bound: an item of one block takes 4.9 us, mostly its queries' copy, which waits for the
+// last item's last Q K^T; a further block 1.5 to 1.7 us, the tiles' softmax and MMAs in
+// turn, with 64 KB of Keys and Values an SM out of L2 (6 TB/s).  Tried: the next queries
+// prefetched into L2 (512 states 115 us), the next Keys waited for earlier (114).
+//
 // Few items of many states are split over a cluster (p.split CTAs, an equal run of
 // blocks each), whose outputs, maxima and sums meet through distributed shared
 // memory, in rank order.
@@ -34,14 +43,17 @@ namespace {
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kMmaWarp = 8, kCopyWarp = 9, kOutWarp = 12;
+// Warps that write outputs.
+template <int D, bool SPLIT>
+constexpr bool kOutWarps = D == 128 && !SPLIT;
 // Registers a thread after the split of the launch's 4 x 128 (3 x 168 without output
 // warps): a softmax thread holds a whole row of scores.
-template <bool SPLIT>
-constexpr int kTcThreads = SPLIT ? 384 : 512;
-template <bool SPLIT>
-constexpr int kSoftmaxRegs = SPLIT ? 216 : 176;
-template <bool SPLIT>
-constexpr int kOtherRegs = SPLIT ? 72 : 88;
+template <bool OUT>
+constexpr int kTcThreads = OUT ? 512 : 384;
+template <bool OUT>
+constexpr int kSoftmaxRegs = OUT ? 176 : 216;
+template <bool OUT>
+constexpr int kOtherRegs = OUT ? 88 : 72;
 constexpr int kOutRegs = 72;
 constexpr float kSlack = 8.f;
 
@@ -71,7 +83,7 @@ struct TcLayout {
   static constexpr uint32_t kTile = kChunk * (D / 64);    // a Q, K or V tile
   static constexpr uint32_t kStageWarp = 32 * 128;        // 32 rows of 64 output channels
   static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kStage = kRing + kSlots * kTile, kBars = kStage + 8 * kStageWarp;
-  static constexpr uint32_t kMl = kStage + 4 * kStageWarp;  // [tile][row] (m, l), behind the output warps' stages
+  static constexpr uint32_t kMl = kStage + 4 * kStageWarp;  // [tile][row] (m, l), behind four output warps' stages
   // barriers: full and empty per slot, the end, then per tile: Q full, Q empty, S, P (two halves), O after a block, S
   // read, O after an item, (m, l) written, O read
   static constexpr int kNBars = 2 * kSlots + 1 + 20;
@@ -118,11 +130,52 @@ struct Brief {
   uint32_t info;  // states of the last block, tile 1 has tokens (bit 8), another item follows (bit 9)
 };
 
+// A warp's rows of an item's output, from tensor memory at ``to``, 64 channels at a time
+// through shared memory, 16-byte pieces swizzled by row, so that it stores whole rows.
+// free_bar (or 0): told once tensor memory has been read.
+template <int D>
+__device__ __forceinline__ void write_rows(const CrossParams& p, const Item& it, int pos, int head, bool live,
+                                           uint32_t rows_live, uint32_t to, uint8_t* stage, float inv, float lse,
+                                           uint32_t free_bar) {
+  const int lane = threadIdx.x & 31;
+  __nv_bfloat16* dst =
+      static_cast<__nv_bfloat16*>(p.out) + (int64_t)(it.seq.q_start + pos) * p.o_ts + (int64_t)head * p.o_hs;
+#pragma unroll 1
+  for (int half = 0; half < D / 64; ++half) {
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      float o[32];
+      tm_ld32(to + 64 * half + 32 * c, o);  // (without states anything, and not used)
+      tm_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = it.n > 0 ? o[e] * inv : 0.f;
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((4 * c + e / 8) ^ (lane & 7)) * 16) =
+            make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
+                       pack_bf16(o[e + 6], o[e + 7]));
+    }
+    tm_fence_before();
+    if (half == D / 64 - 1 && free_bar) warp_arrive(free_bar);
+    __syncwarp();
+#pragma unroll
+    for (int y = lane; y < 32 * 8; y += 32) {
+      const int row = y / 8, c = y % 8;
+      const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (c ^ (row & 7)) * 16);
+      if (rows_live >> row & 1u) *reinterpret_cast<uint4*>(at + 128 * half + 16 * c) = v;
+    }
+    __syncwarp();
+  }
+  if (live && p.lse) p.lse[(int64_t)head * p.n_tokens + it.seq.q_start + pos] = lse;
+}
+
 // SPLIT: a cluster of p.split CTAs an item, one item a cluster; else items in turn.
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
+__global__ void __launch_bounds__(kTcThreads<kOutWarps<D, SPLIT>>, 1)
     cross_tc_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ TcMaps maps, int n_items) {
   using L = TcLayout<D>;
+  constexpr bool OUT = kOutWarps<D, SPLIT>;
   extern __shared__ uint8_t tc_raw[];
   uint8_t* smem = tc_raw + ((1024u - (smem_u32(tc_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -166,7 +219,7 @@ __global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
   pdl_release();
 
   if (warp >= kMmaWarp && warp < kOutWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<SPLIT>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<OUT>));
     if (warp == kCopyWarp) {
       // ============ copies (lane 0): per item Q_0, Q_1, then K_0, V_0, K_1, V_1 ... ====
       if (lane == 0) {
@@ -302,7 +355,7 @@ __global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
                          j > 0 || ks > 0);
               };
               ok = ok && bar_wait(bar_p + 16 * i, ph_p >> i & 1u, abort);
-              if (!SPLIT && j == 0) {  // O_i has been read
+              if (OUT && j == 0) {  // O_i has been read
                 if (used >> i & 1u) {
                   ok = ok && bar_wait(bar_free + 8 * i, ph_f >> i & 1u, abort);
                   ph_f ^= 1u << i;
@@ -352,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
     }
   } else if (warp < kMmaWarp) {
     // ============ softmax: tile i, one row a thread ===================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<SPLIT>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<OUT>));
     const int i = warp >> 2, r = t & 127;
     const int tt = r / p.g;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -372,7 +425,7 @@ __global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
         kv_len = it.seq.kv_len;
         warp_live = __any_sync(0xffffffffu, tt < tile_tok && it.tok0 + i * tile_tok + tt < it.seq.q_len);
       }
-      if (n == 0 && !SPLIT) continue;
+      if (n == 0 && OUT) continue;
       float m = -FLT_MAX, l = 0.f;  // (not -INFINITY: scores of minus infinity may come first)
       auto before_weights = [&](int j) {  // the last block's P V, or the last item's, is done with P (and with O)
         bool done = true;
@@ -453,11 +506,23 @@ __global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
         if (n > 0 && !(ok = warp_wait(bar_e + 8 * i, 0, abort))) break;
         tm_fence_after();
         ml[t] = make_float2(m, l);
-      } else {
+      } else if constexpr (OUT) {
         // the last item's have been read (else its phase of bar_l could pass unseen, too)
         if (n_e > 0 && !(ok = warp_wait(bar_free + 8 * i, (n_e - 1) & 1u, abort))) break;
         ml[t] = make_float2(m, l);
         warp_arrive(bar_l + 8 * i);
+      } else {
+        if (n > 0 && !(ok = warp_wait(bar_e + 8 * i, n_e & 1u, abort))) break;
+        if (warp_live) {
+          tm_fence_after();
+          const Item it = item_at<SPLIT>(p, x);  // (again: kept over the blocks it would cost them registers)
+          const int pos = it.tok0 + i * tile_tok + tt, head = it.head * p.g + r - tt * p.g;
+          const bool live = tt < tile_tok && pos < it.seq.q_len;
+          write_rows<D>(p, it, pos, head, live, __ballot_sync(0xffffffffu, live), to,
+                        smem + L::kStage + warp * L::kStageWarp, 1.f / l,
+                        n > 0 ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY, 0u);
+        }
+        if (n == 0) continue;  // (no phase of this item)
       }
       ++n_e;
     }
@@ -520,7 +585,7 @@ __global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
       cluster_sync();  // no CTA ends while another reads its outputs
     }
   } else {
-    // ============ outputs: an item's O_0, then its O_1, one row a thread =================
+    // ============ outputs (OUT): an item's O_0, then its O_1, one row a thread ============
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     const int r = t & 127, tt = r / p.g, member = r - tt * p.g;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -545,41 +610,8 @@ __global__ void __launch_bounds__(kTcThreads<SPLIT>, 1)
           lse = (row.x + log2f(row.y)) * 0.69314718055994530942f;
         }
         if (rows_live) {
-          __nv_bfloat16* dst =
-              static_cast<__nv_bfloat16*>(p.out) + (int64_t)(it.seq.q_start + pos) * p.o_ts + (int64_t)head * p.o_hs;
-          const uint32_t to = tm + L::kColO + D * i + lanes;
-          // 64 channels at a time through shared memory, 16-byte pieces swizzled by row,
-          // so that the warp stores whole rows
-#pragma unroll 1
-          for (int half = 0; half < D / 64; ++half) {
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              float o[32];
-              tm_ld32(to + 64 * half + 32 * c, o);  // (without states anything, and not used)
-              tm_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = it.n > 0 ? o[e] * inv : 0.f;
-#pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(stage + lane * 128 + ((4 * c + e / 8) ^ (lane & 7)) * 16) =
-                    make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
-                               pack_bf16(o[e + 6], o[e + 7]));
-            }
-            if (half == D / 64 - 1 && it.n > 0) {
-              tm_fence_before();
-              warp_arrive(bar_free + 8 * i);  // O_i has been read
-            }
-            __syncwarp();
-#pragma unroll
-            for (int y = lane; y < 32 * 8; y += 32) {
-              const int row = y / 8, c = y % 8;
-              const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (c ^ (row & 7)) * 16);
-              if (rows_live >> row & 1u) *reinterpret_cast<uint4*>(at + 128 * half + 16 * c) = v;
-            }
-            __syncwarp();
-          }
-          if (live && p.lse) p.lse[(int64_t)head * p.n_tokens + it.seq.q_start + pos] = lse;
+          write_rows<D>(p, it, pos, head, live, rows_live, tm + L::kColO + D * i + lanes, stage, inv, lse,
+                        it.n > 0 ? bar_free + 8 * i : 0u);
         } else if (it.n > 0) {
           warp_arrive(bar_free + 8 * i);
         }
@@ -604,7 +636,7 @@ cudaError_t launch_tc(const CrossParams& p, const TcMaps& maps, int64_t tiles, i
   const cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)TcLayout<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_cluster(cross_tc_kernel<D, SPLIT>, SPLIT || tiles < n_sm ? tiles : n_sm, p.split, kTcThreads<SPLIT>,
+  return launch_cluster(cross_tc_kernel<D, SPLIT>, SPLIT || tiles < n_sm ? tiles : n_sm, p.split, kTcThreads<kOutWarps<D, SPLIT>>,
                         TcLayout<D>::kSmem, s, p, maps, (int)tiles);
 }
 
@@ -616,7 +648,7 @@ int split_of(int64_t tiles, int32_t max_kv, int n_sm) {
   const int64_t blocks = (max_kv + kKeys - 1) / kKeys;
   for (int split = 8; split > 1; --split)
     if (tiles * split <= n_sm && blocks >= 2 * split &&
-        tiles <= active_clusters<cross_tc_kernel<D, true>>(split, kTcThreads<true>, TcLayout<D>::kSmem))
+        tiles <= active_clusters<cross_tc_kernel<D, true>>(split, kTcThreads<false>, TcLayout<D>::kSmem))
       return split;
   return 1;
 }
