@@ -253,7 +253,8 @@ cudaError_t launch_r(const CrossParams& p, int64_t tiles, cudaStream_t s) {
                                              (int)few_smem<T>(kMaxDim));
   if (e != cudaSuccess) return e;
   if (p.split > 8) {
-    const cudaError_t wide = cudaFuncSetAttribute(cross_few_kernel<T, R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t wide =
+        cudaFuncSetAttribute(cross_few_kernel<T, R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (wide != cudaSuccess) return wide;
     if (active_clusters<cross_few_kernel<T, R>>(p.split, kThreads, few_smem<T>(p.D), p.D / 16) < tiles) {
       CrossParams q = p;

@@ -155,7 +155,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     uint32_t pa[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // row gid + 8 i: states 2 tig, 2 tig + 1 and those + 8
-      float x[4] = {s[0][2 * i] * p.scale2, s[0][2 * i + 1] * p.scale2, s[1][2 * i] * p.scale2, s[1][2 * i + 1] * p.scale2};
+      float x[4] = {s[0][2 * i], s[0][2 * i + 1], s[1][2 * i], s[1][2 * i + 1]};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= p.scale2;
       if (limit < kRun) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -268,7 +270,8 @@ cudaError_t launch_rows(const CrossParams& p, const RowsMaps& maps, int64_t tile
                                              (int)RowsLayout<D>::kSmem);
   if (e != cudaSuccess) return e;
   if (p.split > 8) {
-    const cudaError_t wide = cudaFuncSetAttribute(cross_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t wide =
+        cudaFuncSetAttribute(cross_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (wide != cudaSuccess) return wide;
     if (active_clusters<cross_rows_kernel<D>>(p.split, kRowsThreads, RowsLayout<D>::kSmem) < tiles) {
       CrossParams q = p;

@@ -88,7 +88,7 @@ struct TcLayout {
   // read, O after an item, (m, l) written, O read
   static constexpr int kNBars = 2 * kSlots + 1 + 20;
   static constexpr bool kApart = D == 64;                 // P beside S, not over it
-  static constexpr uint32_t kBriefs = kBars + kNBars * 8 + 8;     // behind the tensor memory's address and the abort word
+  static constexpr uint32_t kBriefs = kBars + kNBars * 8 + 8;  // behind the tensor memory's address and the abort word
   static constexpr size_t kSmem = kBriefs + 16 + 1024;    // + alignment
   // S_i at 128 i, O_i at 256 + D i, P_i over S_i or at 384 + 64 i
   static constexpr uint32_t kColS = 0, kColO = 256, kColP = kApart ? 384 : 0, kStepP = kApart ? 64 : 128;
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kTcThreads<kOutWarps<D, SPLIT>>, 1)
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t bar_full = sbase + L::kBars, bar_empty = bar_full + 8 * L::kSlots;
   const uint32_t bar_end = bar_empty + 8 * L::kSlots, bar_q = bar_end + 8, bar_qfree = bar_q + 16,
-                 bar_s = bar_qfree + 16, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16, bar_e = bar_r + 16, bar_l = bar_e + 16, bar_free = bar_l + 16;
+                 bar_s = bar_qfree + 16, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_r = bar_o + 16, bar_e = bar_r + 16,
+                 bar_l = bar_e + 16, bar_free = bar_l + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * L::kNBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   Brief* briefs = reinterpret_cast<Brief*>(smem + L::kBriefs);
@@ -636,8 +637,8 @@ cudaError_t launch_tc(const CrossParams& p, const TcMaps& maps, int64_t tiles, i
   const cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)TcLayout<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_cluster(cross_tc_kernel<D, SPLIT>, SPLIT || tiles < n_sm ? tiles : n_sm, p.split, kTcThreads<kOutWarps<D, SPLIT>>,
-                        TcLayout<D>::kSmem, s, p, maps, (int)tiles);
+  return launch_cluster(cross_tc_kernel<D, SPLIT>, SPLIT || tiles < n_sm ? tiles : n_sm, p.split,
+                        kTcThreads<kOutWarps<D, SPLIT>>, TcLayout<D>::kSmem, s, p, maps, (int)tiles);
 }
 
 template <int D>

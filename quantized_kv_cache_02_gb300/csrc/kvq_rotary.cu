@@ -258,7 +258,8 @@ uint64_t turns_of(double f) {
   const double hi = f * kInv, lo = std::fma(f, kInv, -hi) + f * kInvRest;
   double part = hi - std::nearbyint(hi);  // exact, in [-1/2, 1/2]
   if (part == 0.5) part = -0.5;           // the same angle, and 2^63 would not fit
-  return (uint64_t)(int64_t)std::nearbyint(std::ldexp(part, 64)) + (uint64_t)(int64_t)std::nearbyint(std::ldexp(lo, 64));
+  auto fixed = [](double x) { return (uint64_t)(int64_t)std::nearbyint(std::ldexp(x, 64)); };
+  return fixed(part) + fixed(lo);
 }
 
 kvq_status rotary(const kvq_rotary_plan* plan, const void* positions, int32_t position_bytes,
@@ -336,7 +337,9 @@ kvq_status rotary(const kvq_rotary_plan* plan, const void* positions, int32_t po
   // As many tokens a block as leave enough blocks (and its threads fit), then the heads
   // side by side; with few tokens the heads are split among blocks too.
   p.tokens = 1;
-  while (2 * p.tokens * p.items <= kRotaryThreads && 2 * p.tokens * p.pairs <= kMaxAngles && n_tokens >= 2 * p.tokens * kBlocksPerSm * (int64_t)n_sm) p.tokens *= 2;
+  while (2 * p.tokens * p.items <= kRotaryThreads && 2 * p.tokens * p.pairs <= kMaxAngles &&
+         n_tokens >= 2 * p.tokens * kBlocksPerSm * (int64_t)n_sm)
+    p.tokens *= 2;
   p.lanes = std::min(p.heads, kRotaryThreads / (p.tokens * p.items));
   const int64_t blocks = (n_tokens + p.tokens - 1) / p.tokens;
   if (blocks > kMaxTiles) return fail(KVQ_EUNSUPPORTED, "too many tokens for one launch");
