@@ -20,10 +20,12 @@
 // themselves (they are slower with the registers that four more warps leave them: 2048
 // states 171 us, 160 without).
 //
-// Bound: an item of one block takes 4.9 us, mostly its queries' copy, which waits for the
-// last item's last Q K^T; a further block 1.5 to 1.7 us, the tiles' softmax and MMAs in
-// turn, with 64 KB of Keys and Values an SM out of L2 (6 TB/s).  Tried: the next queries
-// prefetched into L2 (512 states 115 us), the next Keys waited for earlier (114).
+// Bound: an item of one block takes 4.9 us (its two tiles' scores, softmax, output and
+// copies, one after the other with little under them), a further block 1.5 to 1.7 us: the
+// tiles' softmax and MMAs in turn, with 64 KB of Keys and Values an SM out of L2 (6 TB/s).
+// Tried: the next queries prefetched into L2 (512 states 115 us), or copied into ring
+// slots as they come free, a block or more earlier (114); the next Keys waited for
+// earlier (114).
 //
 // Few items of many states are split over a cluster (p.split CTAs, an equal run of
 // blocks each), whose outputs, maxima and sums meet through distributed shared
